@@ -283,6 +283,125 @@ int wan_block_causal_attn_pair_splits(int B, int Lq, int Lk, int heads,
  * negative wan_status on failure.                                          */
 int wan_attn_pair_resident_clusters(void);
 
+/* ------------------------------------------------ paged K / V cache -----
+ * Long-video survey (atlascloud.ai), section "Route 3 · Self Forcing": video
+ * is generated chunk after chunk, each chunk attending to the earlier ones
+ * through a KV cache that may be capped at a number of frames.  These calls
+ * serve several such streams at once, of different lengths and
+ * resolutions: their keys and values live in pages of one pool, found
+ * through a block table per stream, and every length stays on the device,
+ * so a step can be captured into a CUDA graph and replayed with other
+ * lengths.  A step is one wan_paged_plan, then for every layer (and every
+ * denoising pass over the same chunk) wan_paged_write and wan_paged_attn.
+ * The pages have no counterpart of the paging itself; what the attention
+ * sees is wan_block_causal_attn's rule plus the window.
+ *
+ * Layouts.  The new tokens of all streams are packed: the rows of stream r
+ * follow those of stream r - 1, q and o [token_cap, heads, 128], k and v
+ * [token_cap, kv_heads, 128] bf16.  Query head h reads the keys of head
+ * h / (heads / kv_heads).  A layer's pools are [n_pages, kv_heads,
+ * page_size, 128] bf16 each for K and V: one head's part of a page is
+ * contiguous.  Position a of stream r lives at row a % page_size of page
+ * block_table[r][a / page_size].  All device pointers are 16-byte aligned.
+ *
+ * wan_stream_t: settings of a stream.  H x W tokens a frame; position a is
+ * frame a / (H W), row a % (H W) / W, column a % W.  A query at position a
+ * sees keys max(0, e - window_tokens) <= j < min(kv_len, e), with
+ * e = (a / chunk_tokens + 1) * chunk_tokens: its own chunk and the earlier
+ * ones, the last window_tokens positions up to its chunk's end only
+ * (window_tokens 0: all).  chunk_tokens 1 is causal by token.
+ * wan_token_t: one packed row: its position on the three axes and its slot,
+ * page * page_size + row in the page; slot -1: the row takes no part.      */
+typedef struct {
+  int32_t H, W, chunk_tokens, window_tokens;
+} wan_stream_t;
+
+typedef struct {
+  int32_t t, h, w, slot;
+} wan_token_t;
+
+/* Sizes (host) and device arrays of a cache; all arrays are the caller's. */
+typedef struct {
+  int32_t n_streams;      /* R: 1..1024                                     */
+  int32_t max_pages;      /* block table entries of a stream                */
+  int32_t n_pages;        /* pages in the pool                              */
+  int32_t page_size;      /* 16, 32, 64 or 128 tokens                       */
+  int32_t token_cap;      /* packed rows of q, k, v and o                   */
+  int32_t max_new;        /* most new tokens of one stream in a step; the
+                             same value in the plan and the calls using it */
+  int32_t heads, kv_heads;
+  wan_grid_t grid;        /* largest position + 1 on each axis: the grid of
+                             the RoPE table                                 */
+  const wan_stream_t* streams;  /* [R]                                      */
+  /* state, carried from step to step */
+  int32_t* kv_lens;       /* [R] tokens of the stream so far                */
+  int32_t* first_pages;   /* [R] leading table entries already given back   */
+  int32_t* block_table;   /* [R][max_pages], -1: no page                    */
+  int32_t* free_ring;     /* [n_pages] ring of free pages                   */
+  int32_t* ring_state;    /* [2] index of the first free page, their count  */
+  /* written by wan_paged_plan */
+  int32_t* q_start;       /* [R + 1] first packed row of each stream        */
+  int32_t* q_lens;        /* [R] rows that take part (0: refused, idle)     */
+  int32_t* status;        /* [R] WAN_OK, WAN_EINVAL or WAN_ENOSPACE         */
+  wan_token_t* tokens;    /* [token_cap]                                    */
+  int32_t* work;          /* wan_paged_work_bytes(R) bytes: the attention's
+                             division of the step's work, zero at first    */
+} wan_paged_t;
+
+/* Bytes of wan_paged_t.work (0 for a bad count). */
+size_t wan_paged_work_bytes(int n_streams);
+
+/* Plans a step from new_lens (device, [R]): > 0 new tokens of the stream,
+ * 0 none, < 0 the stream has ended.  In this order:
+ *   1. An ended stream's pages go back to the ring and its length to 0.  A
+ *      stream with new tokens gives back the pages that lie wholly before
+ *      what its first new token sees.  Their table entries become -1.
+ *   2. A stream's new tokens are refused with WAN_EINVAL if its settings are
+ *      out of range (H, W, chunk_tokens >= 1, window_tokens >= 0), it would
+ *      pass max_pages pages or the grid, its rows would pass token_cap, or
+ *      it brings more than max_new; nothing of it changes.
+ *   3. The others take pages from the ring in the order of the streams, up
+ *      to the first that the free pages do not suffice for: it and all
+ *      after it are refused with WAN_ENOSPACE (they keep what they have and
+ *      can be planned again).  Pages given back in 1. count as free.
+ * A refused stream's rows keep their place in the packing with slot -1.
+ * Writes kv_lens (including the new tokens), first_pages, block_table,
+ * free_ring, ring_state, q_start, q_lens, status, tokens (all token_cap of
+ * them) and work.  A free ring starts as pages 0 .. n_pages - 1 with
+ * ring_state {0, n_pages}, lengths and first pages 0, table entries -1.
+ * One launch; plans of one cache must not overlap on the device.           */
+int wan_paged_plan(const wan_paged_t* c, const int32_t* new_lens, void* s);
+
+/* Writes the planned tokens: t <- rope3d(t / sqrt(mean(t^2) + eps) * w) for
+ * q (mean over heads * 128, weights wq, result to q_out, which may be q)
+ * and k (mean over kv_heads * 128, weights wk, result to its slot in
+ * k_pages); v goes to its slot in v_pages unchanged.  The rotation is that
+ * of wan_qk_norm_rope at the row's (t, h, w), with the table of c->grid.
+ * Only c->tokens is read of the plan: a row whose slot is not in
+ * [0, n_pages * page_size) or whose position is outside the grid is left
+ * out (its q_out row stays as it was).  The slots of a call must differ.
+ * q, k and v must not overlap the pools.                                   */
+int wan_paged_write(const wan_paged_t* c, const void* q, void* q_out,
+                    const void* k, const void* v, const float* wq,
+                    const float* wk, void* k_pages, void* v_pages,
+                    const void* d_table, float eps, void* s);
+
+/* o = softmax(q K^T * softmax_scale) V for the planned rows, over the pages.
+ * The rows of stream r are its last q_lens[r] positions; a row that sees no
+ * key gives 0.  Rows of no stream (refused, or behind the last one) are left
+ * as they were.  A table entry outside [0, n_pages) reads as keys and values
+ * of zero; positions of a page that no row of the work item sees (behind
+ * the stream's end, or before its window) may hold anything, NaN included.
+ * fp32 softmax and accumulation; the weights are rounded to bf16 for the
+ * tensor cores.  o must not alias q or the pools.
+ * workspace: wan_paged_workspace_bytes(c) bytes of device memory, 16-byte
+ * aligned, contents free on entry and unspecified on return; calls that
+ * share one must not overlap on the device.                                */
+size_t wan_paged_workspace_bytes(const wan_paged_t* c);
+int wan_paged_attn(const wan_paged_t* c, const void* q, const void* k_pages,
+                   const void* v_pages, void* o, float softmax_scale,
+                   void* workspace, size_t workspace_bytes, void* s);
+
 /* ---------------------------------------- block prologue and epilogue --
  * Wan2.2 source reading, ch. 4, section "Full forward of one block": the
  * self-attention input is norm1(x) * (1 + e[1]) + e[0] and the block output

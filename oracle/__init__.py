@@ -25,6 +25,7 @@ Modules:
 * ``step``      -- classifier-free-guidance combine and Euler flow step;
 * ``block``     -- AdaLN modulate, QK-Norm + RoPE, gated residual around the
   attention;
+* ``paged``     -- paged K / V cache: plan of a step, write, attention;
 * ``unipc``     -- the UniPC order-2 predictor-corrector sampler step (the
   pages give no coefficients: written from the published UniPC order
   conditions, pinned by exactness and convergence order).
@@ -38,3 +39,4 @@ preservation); the readings taken are listed in ``rope``'s docstring.
 """
 
 from . import grid, rope, attention, schedule, step, block, unipc  # noqa: F401,E501
+from . import paged  # noqa: F401

@@ -2079,3 +2079,6 @@ int wan_device_status(int clear) {
 }
 
 }  // extern "C"
+
+// The attention over paged keys and values, built from the pieces above.
+#include "paged_attn.cuh"

@@ -15,7 +15,7 @@
 // All three are HBM-bound passes: one CTA or warp per token, 16-byte
 // accesses, the token's row held in registers (modulate) or re-read from L2
 // (QK-Norm), so each tensor crosses HBM once each way.
-#include "wan_internal.cuh"
+#include "rope_common.cuh"
 
 namespace wan {
 namespace {
@@ -102,33 +102,6 @@ struct NormRopeArgs {
   int L, heads, F, H, W;
   float eps;
 };
-
-__device__ __forceinline__ float2 bf16x2_to_float2(uint32_t v) {
-  float2 r;
-  r.x = __uint_as_float(v << 16);
-  r.y = __uint_as_float(v & 0xFFFF0000u);
-  return r;
-}
-
-__device__ __forceinline__ float4 pair_cs(int p0, const float4* tt,
-                                          const float4* th,
-                                          const float4* tw) {
-  if (p0 + 1 < 22) return __ldg(tt + (p0 >> 1));
-  if (p0 >= 22 && p0 + 1 < 43) return __ldg(th + ((p0 - 22) >> 1));
-  if (p0 >= 44) return __ldg(tw + ((p0 - 42) >> 1));
-  const float4 lo = __ldg(th + 10);
-  const float4 hi = __ldg(tw);
-  return make_float4(lo.x, lo.y, hi.z, hi.w);
-}
-
-// (x * f * w_pair) rotated by {cos, sin}, packed to bf16x2.
-__device__ __forceinline__ uint32_t norm_rot2(uint32_t v, float f, float w0,
-                                              float w1, float co, float si) {
-  const float2 x = bf16x2_to_float2(v);
-  const float a = x.x * f * w0;
-  const float b = x.y * f * w1;
-  return pack_bf16x2(fmaf(a, co, -b * si), fmaf(a, si, b * co));
-}
 
 __global__ void __launch_bounds__(kNrThreads) qk_norm_rope_kernel(
     NormRopeArgs a) {

@@ -1,0 +1,653 @@
+// paged.cu -- the plan of a step over a paged K / V cache and the write of
+// the step's tokens into the pages.
+//
+// Long-video survey (atlascloud.ai), section "Route 3 · Self Forcing": the
+// video grows chunk by chunk against a KV cache that may be capped; Wan2.2
+// source reading, ch. 4, section "3D RoPE": q and k pass an RMSNorm, then
+// turn by the token's frame, row and column.  The calls and their layouts
+// are described in wan.h.
+#include "paged.cuh"
+#include "rope_common.cuh"
+
+namespace wan {
+namespace paged {
+
+int check_cache(const wan_paged_t* c) {
+  if (!c) return WAN_EINVAL;
+  if (c->n_streams < 1 || c->n_streams > kMaxStreams || c->max_pages < 1 ||
+      c->n_pages < 1 || c->n_pages > (1 << 30) || c->token_cap < 1 ||
+      c->token_cap > (1 << 27) || c->max_new < 1 || c->heads < 1 ||
+      c->heads > 1024 || c->kv_heads < 1 || c->heads % c->kv_heads != 0)
+    return WAN_EINVAL;
+  if (c->page_size != 16 && c->page_size != 32 && c->page_size != 64 &&
+      c->page_size != 128)
+    return WAN_EINVAL;
+  const int64_t lim = 1ll << 31;
+  if (static_cast<int64_t>(c->n_streams) * c->max_pages >= lim ||
+      static_cast<int64_t>(c->max_pages) * c->page_size >= lim ||
+      static_cast<int64_t>(c->n_pages) * c->page_size >= lim ||
+      static_cast<int64_t>(c->token_cap) * c->heads >= lim ||
+      (static_cast<int64_t>(c->n_pages) * c->page_size / kStage +
+       2ll * c->n_streams) * c->kv_heads >= lim)
+    return WAN_EINVAL;
+  if (wan_rope3d_table_bytes(c->grid, 128) == 0) return WAN_EINVAL;
+  const void* all[] = {c->streams,    c->kv_lens, c->first_pages,
+                       c->block_table, c->free_ring, c->ring_state,
+                       c->q_start,    c->q_lens,  c->status,
+                       c->tokens,     c->work};
+  for (const void* p : all)
+    if (!p) return WAN_EINVAL;
+  for (const void* p : all)
+    if (!aligned16(p)) return WAN_EALIGN;
+  return WAN_OK;
+}
+
+namespace {
+
+// ------------------------------------------------------------- the plan --
+//
+// One cluster of CTAs.  Every CTA reads all streams (one thread a stream)
+// and finds the same prefix sums; the moves of pages and the tokens' records
+// are then spread over the threads of all CTAs, each finding its stream by a
+// binary search of the sums.  Pages come back to the ring's tail and leave
+// from its head, which never meet: what the ring holds and what the streams
+// hold add up to n_pages.  One cluster barrier separates the reads of the
+// old state and the pages coming back from the writes of the new state and
+// the pages going out, so no second launch is needed and no CTA waits for
+// another kernel.
+constexpr int kPlanThreads = 1024;
+
+struct PlanArgs {
+  wan_paged_t c;
+  const int32_t* new_lens;
+  int page_shift;
+  int sms;
+  int few;
+};
+
+__device__ __forceinline__ uint64_t block_scan(uint64_t v, uint64_t* red) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint64_t u = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += u;
+  }
+  __syncthreads();  // red is reused by consecutive calls
+  if (lane == 31) red[warp] = v;
+  __syncthreads();
+  if (warp == 0) {
+    uint64_t t = red[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint64_t u = __shfl_up_sync(0xffffffffu, t, o);
+      if (lane >= o) t += u;
+    }
+    red[lane] = t;
+  }
+  __syncthreads();
+  return warp ? v + red[warp - 1] : v;
+}
+
+// First r in [0, n) with incl[r] > x (n - 1 if there is none).
+__device__ __forceinline__ int find_stream(const int* incl, int n, int x) {
+  int lo = 0, hi = n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (incl[mid] > x)
+      hi = mid;
+    else
+      lo = mid + 1;
+  }
+  return lo;
+}
+
+// Makespan of a division of the tile kernel's work, in 128-key blocks, and
+// the constants it is estimated with: a unit costs its blocks and about 3
+// more (Q load, first scores, output), a split call 2 more for the combining
+// pass and 1/50 for each partial result (133 KB written and read at memory
+// speed).
+constexpr int kUnitCost = 3;
+constexpr int kJoinCost = 2;
+constexpr int kSlotsPerBlock = 50;
+constexpr int kMinRange = 8;  // key blocks of a range
+
+// The attention's work list, by one CTA.  ql and kv are stream threadIdx.x's
+// rows and keys.
+__device__ void build_work(const PlanArgs& a, int ql, int kv, int chunk,
+                           int window, uint64_t* red, int* s_a, int* s_b,
+                           int* s_c, int64_t* s_cost) {
+  const wan_paged_t& c = a.c;
+  const int r = threadIdx.x;
+  int32_t* work = c.work;
+  const bool on = ql > 0;
+  const int lo = on ? key_lo(kv - ql, chunk, window) : 0;
+  if (a.few) {
+    // 64-key stages from the first row's first key to the end; at least one,
+    // so that rows that see nothing are written too
+    int n = 0;
+    if (on) n = (kv + kStage - 1) / kStage - min(lo, kv - 1) / kStage;
+    const uint64_t sc = block_scan(
+        (static_cast<uint64_t>(on) << 40) | static_cast<uint64_t>(n), red);
+    const int idx = static_cast<int>(sc >> 40) - on;
+    const int base = static_cast<int>(sc & 0xFFFFFFFFFFull) - n;
+    if (on) {
+      int32_t* e = work + kHdr + kEnt * idx;
+      e[E_STREAM] = r;
+      e[E_BASE] = base;
+      e[E_COUNT] = n;
+    }
+    if (r == blockDim.x - 1) {
+      const int64_t total = static_cast<int64_t>(base + n) * c.kv_heads;
+      // at least 2 stages a CTA: one stage is a full pipeline latency
+      int64_t ctas = total / 2;
+      const int64_t most = static_cast<int64_t>(a.sms) * kFewCtasPerSm;
+      ctas = ctas < 1 ? 1 : ctas > most ? most : ctas;
+      work[H_MODE] = kModeFew;
+      work[H_ACTIVE] = idx + on;
+      work[H_TOTAL] = static_cast<int>(total);
+      work[H_CTAS] = static_cast<int>(ctas);
+      work[H_ROWS] = 0;
+    }
+    return;
+  }
+  // 128-key blocks of the longest tile (an upper bound under a window)
+  int nb = 0;
+  if (on) {
+    nb = (kv + kBlock - 1) / kBlock - min(lo, kv - 1) / kBlock;
+    if (nb < 1) nb = 1;
+  }
+  // streams by falling length: CTA i takes units i, i + G, ... so its share
+  // is heaviest for i = 0 and within one unit of the lightest
+  s_a[r] = nb;
+  __syncthreads();
+  int rank = 0;
+  for (int i = 0; i < c.n_streams; ++i) {
+    const int o = s_a[i];
+    rank += (o > nb || (o == nb && i < r)) ? 1 : 0;
+  }
+  const int n_act = __syncthreads_count(on);
+  const int tiles = (ql + kTileRows - 1) / kTileRows;
+  __syncthreads();
+  if (on) {
+    s_a[rank] = nb;
+    s_b[rank] = tiles;
+    s_c[rank] = r;
+  }
+  __syncthreads();
+  // warp w tries ranges of at most 1 / (w + 1) of the longest stream
+  const int lane = r & 31, w = r >> 5;
+  const int longest = n_act ? s_a[0] : 0;
+  const int range = (longest + w) / (w + 1);
+  int64_t cost = INT64_MAX;
+  if (n_act && (w == 0 || range >= kMinRange)) {
+    int64_t t = 0, base = 0, slots = 0;
+    for (int i0 = 0; i0 < n_act; i0 += 32) {
+      const int i = i0 + lane;
+      int64_t units = 0;
+      int len = 0, ns = 1;
+      if (i < n_act) {
+        ns = (s_a[i] + range - 1) / range;
+        units = static_cast<int64_t>(s_b[i]) * c.heads * ns;
+        len = (s_a[i] + ns - 1) / ns;
+      }
+      int64_t incl = units;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t u = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += u;
+      }
+      const int64_t p0 = base + incl - units, p1 = base + incl;
+      const int64_t cnt = (p1 + a.sms - 1) / a.sms - (p0 + a.sms - 1) / a.sms;
+      t += cnt * (len + kUnitCost);
+      if (ns > 1) slots += units;
+      base += __shfl_sync(0xffffffffu, incl, 31);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      t += __shfl_xor_sync(0xffffffffu, t, o);
+      slots += __shfl_xor_sync(0xffffffffu, slots, o);
+    }
+    if (slots <= static_cast<int64_t>(a.sms) * kTileSlotsPerSm)
+      cost = kSlotsPerBlock * t + (slots ? kSlotsPerBlock * kJoinCost : 0) +
+             slots;
+  }
+  if (lane == 0) s_cost[w] = cost;
+  __syncthreads();
+  int best = 0;
+  for (int i = 1; i < 32; ++i)
+    if (s_cost[i] < s_cost[best]) best = i;
+  const int rng = (longest + best) / (best + 1);
+  // entry r of the list
+  int ns = 1;
+  uint64_t units = 0, slots = 0, rows = 0;
+  int src = 0;
+  if (r < n_act) {
+    ns = (s_a[r] + rng - 1) / rng;
+    src = s_c[r];
+    units = static_cast<uint64_t>(s_b[r]) * c.heads * ns;
+    if (ns > 1) slots = units;
+  }
+  __syncthreads();
+  s_a[r] = ql;
+  __syncthreads();
+  if (r < n_act && ns > 1)
+    rows = static_cast<uint64_t>(s_a[src]) * c.heads;
+  const uint64_t su = block_scan((units << 32) | slots, red);
+  const uint64_t sr = block_scan(rows, red);
+  if (r < n_act) {
+    int32_t* e = work + kHdr + kEnt * r;
+    e[E_STREAM] = src;
+    e[E_BASE] = static_cast<int>((su >> 32) - units);
+    e[E_COUNT] = s_b[r];
+    e[E_SPLIT] = ns;
+    e[E_SLOT] = static_cast<int>((su & 0xFFFFFFFFull) - slots);
+    e[E_ROW] = static_cast<int>(sr - rows);
+  }
+  if (r == blockDim.x - 1) {
+    work[H_MODE] = kModeTile;
+    work[H_ACTIVE] = n_act;
+    work[H_TOTAL] = static_cast<int>(su >> 32);
+    work[H_CTAS] = a.sms;
+    work[H_ROWS] = static_cast<int>(sr);
+  }
+}
+
+__global__ void __launch_bounds__(kPlanThreads)
+    paged_plan_kernel(const __grid_constant__ PlanArgs a) {
+  __shared__ uint64_t red[32];
+  __shared__ int64_t s_cost[32];
+  __shared__ int s_end[kMaxStreams];    // packed rows up to and with stream r
+  __shared__ int s_rows[kMaxStreams];   // admitted rows
+  __shared__ int s_back[kMaxStreams];   // pages coming back, inclusive
+  __shared__ int s_need[kMaxStreams];   // pages going out, inclusive
+  __shared__ int s_old[kMaxStreams];    // tokens before the step
+  __shared__ int s_from[kMaxStreams];   // first page coming back
+  const wan_paged_t& c = a.c;
+  const int R = c.n_streams;
+  const int r = threadIdx.x;
+  const int ps = c.page_size;
+  const uint32_t np = static_cast<uint32_t>(c.n_pages);
+  const uint32_t head = static_cast<uint32_t>(c.ring_state[0]) % np;
+  const int count =
+      min(max(c.ring_state[1], 0), c.n_pages);
+  int nw = 0, old = 0, first = 0;
+  int4 cfg = make_int4(1, 1, 1, 0);
+  if (r < R) {
+    nw = a.new_lens[r];
+    old = max(c.kv_lens[r], 0);
+    first = max(c.first_pages[r], 0);
+    cfg = reinterpret_cast<const int4*>(c.streams)[r];
+  }
+  const int rows = max(nw, 0);
+  const bool ended = nw < 0;
+  const int64_t end =
+      static_cast<int64_t>(block_scan(static_cast<uint64_t>(rows), red));
+  const int64_t total = static_cast<int64_t>(old) + rows;
+  const int64_t cap = c.token_cap;
+  const bool fit =
+      cfg.x >= 1 && cfg.y >= 1 && cfg.x <= c.grid.H && cfg.y <= c.grid.W &&
+      cfg.z >= 1 && cfg.w >= 0 && rows <= c.max_new &&
+      total <= static_cast<int64_t>(c.max_pages) * ps &&
+      total <= static_cast<int64_t>(c.grid.F) * cfg.x * cfg.y && end <= cap;
+  const bool valid = nw > 0 && fit;
+  // pages held before the step, and those of them that come back
+  const int held = min(static_cast<int>(
+                           (static_cast<int64_t>(old) + ps - 1) >> a.page_shift),
+                       c.max_pages);
+  first = min(first, held);
+  int gone = first;
+  if (ended)
+    gone = held;
+  else if (valid)
+    gone = max(first, min(key_lo(old, cfg.z, cfg.w), old) >> a.page_shift);
+  const int back = gone - first;
+  const int top =
+      valid ? static_cast<int>((total + ps - 1) >> a.page_shift) : held;
+  const int need = valid ? top - held : 0;
+  const uint64_t sums = block_scan(
+      (static_cast<uint64_t>(back) << 32) | static_cast<uint64_t>(need), red);
+  const int back_incl = static_cast<int>(sums >> 32);
+  const int need_incl = static_cast<int>(sums & 0xFFFFFFFFull);
+  s_back[r] = back_incl;
+  s_from[r] = first;
+  s_old[r] = old;
+  s_end[r] = static_cast<int>(end < cap ? end : cap);
+  __syncthreads();
+  const int n_back = s_back[kMaxStreams - 1];
+  const int free_now = min(count + n_back, c.n_pages);
+  const bool admit = valid && need_incl <= free_now;
+  s_need[r] = need_incl;
+  s_rows[r] = admit ? rows : 0;
+  // admission stops for good at the first stream that does not fit, so the
+  // admitted needs are a prefix of the line of needs
+  const int n_out = static_cast<int>(
+      block_scan(admit ? static_cast<uint64_t>(need) : 0ull, red));
+  __shared__ int s_out;
+  if (r == kPlanThreads - 1) s_out = n_out;
+  const int ctas = gridDim.x;
+  const int rank = blockIdx.x;
+  const int step = ctas * kPlanThreads;
+  const int me = rank * kPlanThreads + r;
+  for (int i = me; i < n_back; i += step) {
+    const int q = find_stream(s_back, R, i);
+    const int at = i - (q ? s_back[q - 1] : 0);
+    int32_t* ent = c.block_table +
+                   static_cast<int64_t>(q) * c.max_pages + s_from[q] + at;
+    c.free_ring[(head + static_cast<uint32_t>(count) + i) % np] = *ent;
+    *ent = -1;
+  }
+  __syncwarp();
+  if (ctas > 1)
+    cluster_sync_all();
+  else
+    __syncthreads();
+  const int out = s_out;
+  for (int i = me; i < out; i += step) {
+    const int q = find_stream(s_need, R, i);
+    const int at = i - (q ? s_need[q - 1] : 0);
+    const int p = ((s_old[q] + ps - 1) >> a.page_shift) + at;
+    c.block_table[static_cast<int64_t>(q) * c.max_pages + p] =
+        c.free_ring[(head + i) % np];
+  }
+  // the tokens' records: the page of a new position is either one the stream
+  // held (its table entry does not change) or comes from the ring
+  int4* tok = reinterpret_cast<int4*>(c.tokens);
+  const int n_rows = s_end[R - 1];
+  for (int i = me; i < c.token_cap; i += step) {
+    int4 rec = make_int4(0, 0, 0, -1);
+    if (i < n_rows) {
+      const int q = find_stream(s_end, R, i);
+      // rows of the stream start where those of the one before end
+      const int off = i - (q ? s_end[q - 1] : 0);
+      if (off < s_rows[q]) {
+        const int pos = s_old[q] + off;
+        const int4 f = __ldg(reinterpret_cast<const int4*>(c.streams) + q);
+        const int hw = f.x * f.y;
+        rec.x = pos / hw;
+        const int rest = pos - rec.x * hw;
+        rec.y = rest / f.y;
+        rec.z = rest - rec.y * f.y;
+        const int p = pos >> a.page_shift;
+        const int h0 = (s_old[q] + ps - 1) >> a.page_shift;
+        int page;
+        if (p < h0)
+          page = c.block_table[static_cast<int64_t>(q) * c.max_pages + p];
+        else
+          page = c.free_ring[(head + (q ? s_need[q - 1] : 0) + (p - h0)) % np];
+        rec.w = (page << a.page_shift) + (pos & (ps - 1));
+      }
+    }
+    tok[i] = rec;
+  }
+  const int kv = ended ? 0 : old + (admit ? rows : 0);
+  if (rank == 0) {
+    if (r < R) {
+      c.kv_lens[r] = kv;
+      c.first_pages[r] = ended ? 0 : gone;
+      const int64_t start = end - rows;
+      c.q_start[r] = static_cast<int>(start < cap ? start : cap);
+      c.q_lens[r] = admit ? rows : 0;
+      c.status[r] = (nw > 0 && !fit)        ? WAN_EINVAL
+                    : (valid && !admit)     ? WAN_ENOSPACE
+                                            : WAN_OK;
+      if (r == R - 1) c.q_start[R] = s_end[r];
+    }
+    if (r == 0) {
+      c.ring_state[0] = static_cast<int>((head + out) % np);
+      c.ring_state[1] = free_now - out;
+    }
+  }
+  // the last CTA has no state to write
+  if (rank == ctas - 1) {
+    __syncthreads();
+    build_work(a, admit ? rows : 0, kv, cfg.z, cfg.w, red, s_back, s_need,
+               s_from, s_cost);
+  }
+}
+
+// ------------------------------------------------------------ the write --
+//
+// HBM-bound: every row of q, k and v is read once and written once.  One
+// warp per (row, tensor); lane l holds 16-byte chunk l & 15 of heads l >> 4,
+// l >> 4 + 2, ... in registers (kRows of them), so a row is one batch of
+// independent loads, one reduction and one batch of stores; a head's 256
+// bytes land contiguously in its page.  For more than 2 * 20 heads the row
+// is read twice (the second time from L2).
+constexpr int kWrThreads = 128;
+constexpr int kWrWarps = kWrThreads / 32;
+constexpr int kWrMaxRows = 20;
+
+struct WriteArgs {
+  const uint4* in[3];      // q, k, v
+  uint4* out[3];           // q_out, k_pages, v_pages
+  const float4* w[2];      // weights of q and k
+  const float4* table;     // RoPE rows of 11 float4
+  const int4* tokens;
+  int rows;                // packed rows
+  int heads, kv_heads;
+  int F, H, W;
+  int page_shift;
+  int slots;               // n_pages * page_size
+  float eps;
+};
+
+template <int kRows>
+constexpr int wr_min_blocks() {
+  return kRows <= 4 ? 8 : kRows <= 8 ? 6 : kRows <= 12 ? 5 : 3;
+}
+
+// kRows 0: any head count, two passes over the row.
+template <int kRows>
+__global__ void
+__launch_bounds__(kWrThreads, kRows ? wr_min_blocks<kRows>() : 8)
+    paged_write_kernel(const __grid_constant__ WriteArgs a) {
+  const int lane = threadIdx.x & 31;
+  const int c = lane & 15;
+  const int hsub = lane >> 4;
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * kWrWarps;
+  const int64_t items = 3ll * a.rows;
+  for (int64_t it = static_cast<int64_t>(blockIdx.x) * kWrWarps +
+                    (threadIdx.x >> 5);
+       it < items; it += stride) {
+    const int row = static_cast<int>(it / 3);
+    const int which = static_cast<int>(it - 3ll * row);
+    const int4 tk = __ldg(a.tokens + row);
+    // rows of no stream, and records that no plan writes
+    if (tk.w < 0 || tk.w >= a.slots || static_cast<unsigned>(tk.x) >= a.F ||
+        static_cast<unsigned>(tk.y) >= a.H ||
+        static_cast<unsigned>(tk.z) >= a.W)
+      continue;
+    const int nh = which == 0 ? a.heads : a.kv_heads;
+    // selects, not indexes: a runtime index into the parameters would copy
+    // them to the stack
+    const uint4* in = which == 0 ? a.in[0] : which == 1 ? a.in[1] : a.in[2];
+    uint4* out = which == 0 ? a.out[0] : which == 1 ? a.out[1] : a.out[2];
+    in += static_cast<int64_t>(row) * nh * 16 + c;
+    int64_t hstep = 16;  // uint4 from one head's row to the next
+    if (which == 0) {
+      out += static_cast<int64_t>(row) * nh * 16 + c;
+    } else {
+      const int page = tk.w >> a.page_shift;
+      const int off = tk.w & ((1 << a.page_shift) - 1);
+      hstep = 16ll << a.page_shift;
+      out += static_cast<int64_t>(page) * nh * hstep + off * 16 + c;
+    }
+    uint4 x[kRows ? kRows : 1];
+    float ss = 0.f;
+    auto squares = [&](const uint4& v) {
+      const uint32_t vv[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float2 f = bf16x2_to_float2(vv[e]);
+        ss = fmaf(f.x, f.x, fmaf(f.y, f.y, ss));
+      }
+    };
+    if (kRows) {
+#pragma unroll
+      for (int k = 0; k < kRows; ++k)
+        if (hsub + 2 * k < nh) x[k] = in[(hsub + 2 * k) * 16];
+    }
+    if (which == 2) {
+      if (kRows) {
+#pragma unroll
+        for (int k = 0; k < kRows; ++k)
+          if (hsub + 2 * k < nh) out[(hsub + 2 * k) * hstep] = x[k];
+      } else {
+        for (int h = hsub; h < nh; h += 2) out[h * hstep] = in[h * 16];
+      }
+      continue;
+    }
+    const float4* tt = a.table + static_cast<int64_t>(tk.x) * 11;
+    const float4* th = a.table + static_cast<int64_t>(a.F + tk.y) * 11;
+    const float4* tw = a.table + static_cast<int64_t>(a.F + a.H + tk.z) * 11;
+    const float4 cs0 = pair_cs(4 * c, tt, th, tw);
+    const float4 cs1 = pair_cs(4 * c + 2, tt, th, tw);
+    if (kRows) {
+#pragma unroll
+      for (int k = 0; k < kRows; ++k)
+        if (hsub + 2 * k < nh) squares(x[k]);
+    } else {
+#pragma unroll 4
+      for (int h = hsub; h < nh; h += 2) squares(in[h * 16]);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    const float f = rsqrtf(ss / (128.0f * nh) + a.eps);
+    const float4* wt = (which ? a.w[1] : a.w[0]) + 2 * c;
+    auto turned = [&](const uint4& v, int h) {
+      const float4 w0 = __ldg(wt + h * 32);
+      const float4 w1 = __ldg(wt + h * 32 + 1);
+      return make_uint4(norm_rot2(v.x, f, w0.x, w0.y, cs0.x, cs0.y),
+                        norm_rot2(v.y, f, w0.z, w0.w, cs0.z, cs0.w),
+                        norm_rot2(v.z, f, w1.x, w1.y, cs1.x, cs1.y),
+                        norm_rot2(v.w, f, w1.z, w1.w, cs1.z, cs1.w));
+    };
+    if (kRows) {
+#pragma unroll
+      for (int k = 0; k < kRows; ++k)
+        if (hsub + 2 * k < nh)
+          out[(hsub + 2 * k) * hstep] = turned(x[k], hsub + 2 * k);
+    } else {
+#pragma unroll 4
+      for (int h = hsub; h < nh; h += 2) out[h * hstep] = turned(in[h * 16], h);
+    }
+  }
+}
+
+int page_shift_of(int page_size) {
+  int s = 0;
+  while ((1 << s) < page_size) ++s;
+  return s;
+}
+
+int device_sms(int dev) {
+  int n = 0;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) !=
+      cudaSuccess)
+    return 0;
+  return n;
+}
+
+}  // namespace
+}  // namespace paged
+}  // namespace wan
+
+extern "C" {
+
+size_t wan_paged_work_bytes(int n_streams) {
+  if (n_streams < 1 || n_streams > wan::paged::kMaxStreams) return 0;
+  return sizeof(int32_t) *
+         (wan::paged::kHdr + static_cast<size_t>(wan::paged::kEnt) * n_streams);
+}
+
+int wan_paged_plan(const wan_paged_t* c, const int32_t* new_lens, void* s) {
+  using namespace wan;
+  using namespace wan::paged;
+  int st = check_cache(c);
+  if (st != WAN_OK) return st;
+  if (!new_lens) return WAN_EINVAL;
+  if (!aligned16(new_lens)) return WAN_EALIGN;
+  int dev = 0;
+  if ((st = check_device(&dev)) != WAN_OK) return st;
+  PlanArgs a;
+  a.c = *c;
+  a.new_lens = new_lens;
+  a.page_shift = page_shift_of(c->page_size);
+  a.sms = device_sms(dev);
+  if (a.sms < 1) return WAN_ECUDA;
+  a.few = few_mode(c) ? 1 : 0;
+  cudaLaunchConfig_t cfg = {};
+  // One CTA up to 2,048 records (two a thread); the portable cluster of 8
+  // beyond, where the records' writes take over.
+  const unsigned ctas = c->token_cap <= 2 * kPlanThreads ? 1 : 8;
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(kPlanThreads);
+  cfg.stream = as_stream(s);
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = ctas;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, paged_plan_kernel, a) == cudaSuccess
+             ? WAN_OK
+             : WAN_ECUDA;
+}
+
+int wan_paged_write(const wan_paged_t* c, const void* q, void* q_out,
+                    const void* k, const void* v, const float* wq,
+                    const float* wk, void* k_pages, void* v_pages,
+                    const void* d_table, float eps, void* s) {
+  using namespace wan;
+  using namespace wan::paged;
+  int st = check_cache(c);
+  if (st != WAN_OK) return st;
+  const void* all[] = {q, q_out, k, v, wq, wk, k_pages, v_pages, d_table};
+  for (const void* p : all)
+    if (!p) return WAN_EINVAL;
+  if (!(eps > 0.f) || k_pages == v_pages || q == k || q_out == k ||
+      q_out == v || q_out == k_pages || q_out == v_pages || k == k_pages ||
+      v == v_pages)
+    return WAN_EINVAL;
+  for (const void* p : all)
+    if (!aligned16(p)) return WAN_EALIGN;
+  int dev = 0;
+  if ((st = check_device(&dev)) != WAN_OK) return st;
+  WriteArgs a;
+  a.in[0] = static_cast<const uint4*>(q);
+  a.in[1] = static_cast<const uint4*>(k);
+  a.in[2] = static_cast<const uint4*>(v);
+  a.out[0] = static_cast<uint4*>(q_out);
+  a.out[1] = static_cast<uint4*>(k_pages);
+  a.out[2] = static_cast<uint4*>(v_pages);
+  a.w[0] = reinterpret_cast<const float4*>(wq);
+  a.w[1] = reinterpret_cast<const float4*>(wk);
+  a.table = static_cast<const float4*>(d_table);
+  a.tokens = reinterpret_cast<const int4*>(c->tokens);
+  a.rows = c->token_cap;
+  a.heads = c->heads;
+  a.kv_heads = c->kv_heads;
+  a.F = c->grid.F;
+  a.H = c->grid.H;
+  a.W = c->grid.W;
+  a.page_shift = page_shift_of(c->page_size);
+  a.slots = c->n_pages * c->page_size;
+  a.eps = eps;
+  void (*kern)(WriteArgs) =
+      c->heads <= 8    ? paged_write_kernel<4>
+      : c->heads <= 16 ? paged_write_kernel<8>
+      : c->heads <= 24 ? paged_write_kernel<12>
+      : c->heads <= 2 * kWrMaxRows
+          ? paged_write_kernel<kWrMaxRows>
+          : paged_write_kernel<0>;
+  const int cap =
+      resident_grid(reinterpret_cast<const void*>(kern), kWrThreads, dev);
+  if (cap < 1) return WAN_ECUDA;
+  int64_t blocks = (3ll * a.rows + kWrWarps - 1) / kWrWarps;
+  if (blocks > cap) blocks = cap;
+  kern<<<static_cast<unsigned>(blocks), kWrThreads, 0, as_stream(s)>>>(a);
+  return cudaGetLastError() == cudaSuccess ? WAN_OK : WAN_ECUDA;
+}
+
+}  // extern "C"

@@ -1,0 +1,71 @@
+// paged.cuh -- what the plan of a paged step (paged.cu) and the attention
+// over the pages (paged_attn.cuh) agree on: the division of the step's work
+// that the plan writes into wan_paged_t.work.
+#pragma once
+
+#include "wan_internal.cuh"
+
+namespace wan {
+namespace paged {
+
+constexpr int kMaxStreams = 1024;
+
+// Streams whose rows (new tokens x query heads of one key head) fit one
+// 16-row tile run on the kernel that streams the cache through mma.sync
+// (kFew); longer ones on the 256-row tcgen05 kernel (kTile).
+constexpr int kFewRows = 16;
+constexpr int kModeNone = 0, kModeFew = 1, kModeTile = 2;
+
+// kFew: the (stream, key head, 64-key stage) items form one line that is cut
+// into equal parts, one per CTA.  kTile: units of (256-row tile, head, key
+// range); a stream's 128-key blocks are cut into nsplit ranges.
+constexpr int kStage = 64;
+constexpr int kBlock = 128;
+constexpr int kTileRows = 256;
+constexpr int kFewCtasPerSm = 2;
+constexpr int kTileSlotsPerSm = 4;
+
+// work[0 .. kHdr): header; then kEnt ints per active stream.
+constexpr int kHdr = 16;
+constexpr int kEnt = 8;
+enum : int {
+  H_MODE = 0,     // kMode*
+  H_ACTIVE = 1,   // entries
+  H_TOTAL = 2,    // kFew: stages x key heads; kTile: units
+  H_CTAS = 3,     // kFew: CTAs that share the line
+  H_ROWS = 4      // kTile: (row, head) pairs of split streams
+};
+enum : int {
+  E_STREAM = 0,
+  E_BASE = 1,     // kFew: stages before it; kTile: units before it
+  E_COUNT = 2,    // kFew: its stages; kTile: its 256-row tiles
+  E_SPLIT = 3,    // kTile: key ranges
+  E_SLOT = 4,     // kTile: first partial-result slot (nsplit > 1)
+  E_ROW = 5       // kTile: split (row, head) pairs before it
+};
+
+// First key that the query at position a sees, and one past its last.
+__host__ __device__ __forceinline__ int64_t chunk_end(int a, int chunk) {
+  return (static_cast<int64_t>(a) / chunk + 1) * chunk;
+}
+__host__ __device__ __forceinline__ int key_lo(int a, int chunk, int window) {
+  if (window <= 0) return 0;
+  const int64_t lo = chunk_end(a, chunk) - window;
+  return lo < 0 ? 0 : lo > 0x7FFFFFFF ? 0x7FFFFFFF : static_cast<int>(lo);
+}
+__host__ __device__ __forceinline__ int key_hi(int a, int chunk, int kv) {
+  if (a < 0) return 0;
+  const int64_t e = chunk_end(a, chunk);
+  return e < kv ? (e > 0 ? static_cast<int>(e) : 0) : kv;
+}
+
+inline bool few_mode(const wan_paged_t* c) {
+  return static_cast<int64_t>(c->max_new) * (c->heads / c->kv_heads) <=
+         kFewRows;
+}
+
+// Checks of the sizes and of the pointers every call needs.
+int check_cache(const wan_paged_t* c);
+
+}  // namespace paged
+}  // namespace wan

@@ -98,6 +98,27 @@ int make_map_bf16(CUtensorMap* m, const void* base, int B, int L, int heads,
   return r == CUDA_SUCCESS ? WAN_OK : WAN_EINVAL;
 }
 
+int make_map_pages(CUtensorMap* m, const void* base, int n_pages,
+                   int kv_heads, int page_size, int box_rows) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return WAN_ECUDA;
+  if (box_rows < 1 || box_rows > page_size) return WAN_EINVAL;
+  cuuint64_t dims[4] = {128, static_cast<cuuint64_t>(page_size),
+                        static_cast<cuuint64_t>(kv_heads),
+                        static_cast<cuuint64_t>(n_pages)};
+  const cuuint64_t head = static_cast<cuuint64_t>(page_size) * 128 * 2;
+  cuuint64_t strides[3] = {256, head,
+                           head * static_cast<cuuint64_t>(kv_heads)};
+  cuuint32_t box[4] = {64, static_cast<cuuint32_t>(box_rows), 1, 1};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+                  const_cast<void*>(base), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? WAN_OK : WAN_EINVAL;
+}
+
 }  // namespace wan
 
 extern "C" {

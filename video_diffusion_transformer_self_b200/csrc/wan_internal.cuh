@@ -32,6 +32,12 @@ int resident_grid(const void* kernel, int threads, int dev);
 int make_map_bf16(CUtensorMap* m, const void* base, int B, int L, int heads,
                   int box_rows);
 
+// Tensor map of a [n_pages, kv_heads, page_size, 128] bf16 page pool with a
+// box of box_rows rows x 64 channels of one head of one page (dims: channel,
+// row, head, page), 128-byte swizzle, zero fill past n_pages.
+int make_map_pages(CUtensorMap* m, const void* base, int n_pages,
+                   int kv_heads, int page_size, int box_rows);
+
 inline bool aligned16(const void* p) {
   return (reinterpret_cast<uintptr_t>(p) & 15u) == 0;
 }

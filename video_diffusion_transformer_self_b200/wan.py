@@ -54,8 +54,19 @@ class UniPCCoef(ctypes.Structure):
         return {name: getattr(self, name) for name, _ in self._fields_}
 
 
+class PagedDesc(ctypes.Structure):
+    """wan_paged_t: sizes and device arrays of a paged cache."""
+    _fields_ = [(name, ctypes.c_int32) for name in (
+        "n_streams", "max_pages", "n_pages", "page_size", "token_cap",
+        "max_new", "heads", "kv_heads")] + [("grid", Grid)] + [
+        (name, ctypes.c_void_p) for name in (
+            "streams", "kv_lens", "first_pages", "block_table", "free_ring",
+            "ring_state", "q_start", "q_lens", "status", "tokens", "work")]
+
+
 _P = ctypes.c_void_p
 _I = ctypes.c_int
+_C = ctypes.POINTER(PagedDesc)
 _D = ctypes.POINTER(ctypes.c_double)
 _SIGNATURES = {
     "wan_status_string": (ctypes.c_char_p, [_I]),
@@ -106,6 +117,13 @@ _SIGNATURES = {
                             ctypes.c_int64, _D, _I, _I, _P]),
     "wan_transpose_blocks": (_I, [_P, _P, ctypes.c_int64, ctypes.c_int64,
                                   ctypes.c_int64, _P]),
+    "wan_paged_work_bytes": (ctypes.c_size_t, [_I]),
+    "wan_paged_plan": (_I, [_C, _P, _P]),
+    "wan_paged_write": (_I, [_C, _P, _P, _P, _P, _P, _P, _P, _P, _P,
+                             ctypes.c_float, _P]),
+    "wan_paged_workspace_bytes": (ctypes.c_size_t, [_C]),
+    "wan_paged_attn": (_I, [_C, _P, _P, _P, _P, ctypes.c_float, _P,
+                            ctypes.c_size_t, _P]),
     "wan_attn_pair_resident_clusters": (_I, []),
     "wan_wait_selftest": (_I, [_I, _P]),
     "wan_device_status": (_I, [_I]),
@@ -579,6 +597,50 @@ def transpose_blocks(inp, out, a, b, row_bytes, stream=None):
     _check(lib().wan_transpose_blocks(_ptr(inp), _ptr(out), int(a), int(b),
                                       int(row_bytes), _stream(stream)),
            "wan_transpose_blocks")
+
+
+# ------------------------------------------------------- paged cache ---
+# paged.PagedCache builds the descriptor and checks the tensors; the calls
+# run on the tensors' own device.
+
+def paged_work_bytes(n_streams):
+    """Bytes of wan_paged_t.work."""
+    return lib().wan_paged_work_bytes(int(n_streams))
+
+
+def paged_workspace_bytes(desc, device):
+    """Workspace bytes of wan_paged_attn on a device."""
+    import torch
+    with torch.cuda.device(device):
+        return lib().wan_paged_workspace_bytes(ctypes.byref(desc))
+
+
+def paged_plan(desc, new_lens, stream=None):
+    import torch
+    with torch.cuda.device(new_lens.device):
+        _check(lib().wan_paged_plan(ctypes.byref(desc), _ptr(new_lens),
+                                    _stream(stream)), "wan_paged_plan")
+
+
+def paged_write(desc, q, q_out, k, v, wq, wk, k_pages, v_pages, table, eps,
+                stream=None):
+    import torch
+    with torch.cuda.device(q.device):
+        _check(lib().wan_paged_write(
+            ctypes.byref(desc), _ptr(q), _ptr(q_out), _ptr(k), _ptr(v),
+            _ptr(wq), _ptr(wk), _ptr(k_pages), _ptr(v_pages), _ptr(table),
+            eps, _stream(stream)), "wan_paged_write")
+
+
+def paged_attn(desc, q, k_pages, v_pages, o, softmax_scale, workspace,
+               stream=None):
+    import torch
+    with torch.cuda.device(q.device):
+        _check(lib().wan_paged_attn(
+            ctypes.byref(desc), _ptr(q), _ptr(k_pages), _ptr(v_pages),
+            _ptr(o), softmax_scale, _ptr(workspace),
+            workspace.numel() * workspace.element_size(), _stream(stream)),
+            "wan_paged_attn")
 
 
 def attn_pair_resident_clusters():
