@@ -116,3 +116,153 @@ def test_few_rows_peaked_softmax():
     steps = [[16]] * 40
     _run(streams, (80, 8, 8), 32, 2, 2, steps, 7, 16, 30, check=(39,),
          q_scale=8.0)
+
+
+# ------------------------------------------------------------- row tiles --
+
+@pytest.mark.parametrize("ps", [16, 32, 64, 128])
+@pytest.mark.parametrize("heads,kv_heads", [(1, 1), (4, 2), (6, 1)])
+def test_tiles_ragged_streams(ps, heads, kv_heads):
+    # rows around a tile and a tile pair, idle and ended streams, single
+    # rows among long ones
+    streams = [(4, 5, 20, 0)] * 7
+    _run(streams, (60, 4, 5), ps, heads, kv_heads,
+         ([17, 1, 128, 129, 0, 256, 257], [300, 127, 1, 20, 255, -1, 3],
+          [40, 513, -1, 1, 2, 5, 0]), 500 + ps, 600, 260)
+
+
+@pytest.mark.parametrize("window,chunk", [(0, 1), (0, 20), (40, 20), (7, 20),
+                                          (300, 60), (130, 1), (0, 2 ** 31 - 1)])
+def test_tiles_windows_and_chunks(window, chunk):
+    streams = [(4, 5, chunk, window), (5, 5, chunk, window)]
+    _run(streams, (80, 5, 5), 16, 2, 2,
+         ([300, 31], [17, 170], [333, 400], [1, 90]), 700 + window, 400, 220)
+
+
+@pytest.mark.parametrize("kv", [127, 128, 129, 255, 257, 2000])
+def test_tiles_one_row_tile_over_a_cache(kv):
+    # the cache first, then 17 rows: ranges of the keys are joined
+    streams = [(5, 10, 50, 0)]
+    _run(streams, (60, 5, 10), 64, 2, 2, ([kv], [17], [33]), kv, 2000, 40,
+         check=(0, 1, 2))
+
+
+def test_tiles_many_units_per_cta():
+    # several units a CTA in every mix of one and two tiles, none visible
+    streams = [(4, 5, 20, 0 if i % 3 else 3) for i in range(40)]
+    new0 = [7 * i % 290 + 1 for i in range(40)]
+    new1 = [11 * i % 270 for i in range(40)]
+    _run(streams, (60, 4, 5), 32, 8, 4, (new0, new1), 900, 300, 900)
+
+
+def test_tiles_peaked_softmax():
+    streams = [(8, 8, 64, 0)]
+    _run(streams, (60, 8, 8), 32, 2, 2, ([700], [500]), 31, 700, 40,
+         q_scale=8.0)
+
+
+def test_tiles_first_keys_hidden_from_some_rows():
+    # rows of one warp whose first block holds no visible key beside rows
+    # whose maximum moves by more than 2^8 a block later
+    streams = [(2, 2, 4, 150)]
+    _run(streams, (400, 2, 2), 16, 1, 1, ([900], [400]), 41, 900, 90,
+         q_scale=8.0)
+
+
+# --------------------------------------------------------- both kernels --
+
+@pytest.mark.parametrize("max_new", [16, 200])
+def test_pages_out_of_range_read_as_zero(max_new):
+    c, oc = make([(4, 4, 16, 0)], (20, 4, 4), 12, 16, 20, 1, 1, 16, max_new)
+    for new in ([16], [16], [16], [10]):
+        want = step(c, oc, new)
+    kp, vp = _fill(c, oc, 5)
+    kp, vp = kp.nan_to_num(), vp.nan_to_num()
+    q = rows_bf16(16, 1, 9).cuda()
+    o = torch.zeros_like(q)
+    for bad in (-1, 12, 2 ** 31 - 1, -2 ** 31):
+        c.block_table[0, 1] = bad
+        c.attn(q, kp, vp, o)
+        torch.cuda.synchronize()
+        kz, vz = kp.clone(), vp.clone()
+        kz[oc.table[0][1]] = 0
+        vz[oc.table[0][1]] = 0
+        (_, rows, ref, mag), = expect_attn(c, oc, q, kz, vz, want, SCALE)
+        assert_attn(f64(o)[rows], ref, mag, "page %d" % bad, 30.0)
+
+
+@pytest.mark.parametrize("max_new,new", [(4, 4), (700, 700)])
+def test_same_result_every_time_and_in_a_graph(max_new, new):
+    streams = [(8, 8, 64, 0)] * 3
+    cap = 3 * 700
+    c, oc = make(streams, (60, 8, 8), 200, 32, 60, 2, 2, cap, 700)
+    step(c, oc, [700, 650, 10])
+    c.max_new = max_new
+    lens = torch.tensor([new, max(1, new // 3), 1], dtype=torch.int32,
+                        device="cuda")
+    kp, vp = c.new_pools()
+    kp.normal_()
+    vp.normal_()
+    q = rows_bf16(cap, 2, 9).cuda()
+    o = torch.zeros_like(q)
+    saved = c.state.clone()
+    c.plan(lens)
+    c.attn(q, kp, vp, o)
+    first = o.clone()
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        c.plan(lens)
+        c.attn(q, kp, vp, o)
+    for _ in range(3):
+        c.state.copy_(saved)
+        o.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(o, first)
+    # other lengths through the same graph
+    lens.copy_(torch.tensor([1, 2, 3], dtype=torch.int32))
+    c.state.copy_(saved)
+    o.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    got = o.clone()
+    want = oc.plan([1, 2, 3])
+    for _, rows, ref, mag in expect_attn(c, oc, q, kp, vp, want, SCALE):
+        assert_attn(f64(got)[rows], ref, mag, "replay", 30.0)
+
+
+def test_write_and_attention_over_layers_match_the_whole_video():
+    """Three chunks of a video through plan, write and attention of two
+    layers give what the contiguous calls give on the whole video."""
+    grid, heads, chunk = (6, 4, 5), 2, 40
+    L = 120
+    g = wan.grid(*grid)
+    table = wan.rope3d_table(g)
+    c, oc = make([(4, 5, chunk, 0)], grid, 9, 16, 9, heads, heads, chunk)
+    kp, vp = c.new_pools(2)
+    w = torch.rand(heads * 128, device="cuda") + 0.5
+    qkv = [[rows_bf16(L, heads, 60 + 3 * i + j).cuda() for j in range(3)]
+           for i in range(2)]
+    outs = [torch.zeros(L, heads, 128, dtype=torch.bfloat16, device="cuda")
+            for _ in range(2)]
+    for i in range(3):
+        step(c, oc, [chunk])
+        part = slice(chunk * i, chunk * (i + 1))
+        for layer in range(2):
+            q, k, v = (x[part].clone() for x in qkv[layer])
+            c.write(q, k, v, w, w, table, kp[layer], vp[layer])
+            o = torch.empty_like(q)
+            c.attn(q, kp[layer], vp[layer], o)
+            outs[layer][part] = o
+    for layer in range(2):
+        q, k, v = (x.clone()[None] for x in qkv[layer])
+        wan.qk_norm_rope(q, k, w, w, g, table)
+        o = torch.empty_like(q)
+        wan.block_causal_attn(q, k, v, o, chunk)
+        torch.cuda.synchronize()
+        # two kernels, each within its bound of the exact value
+        a, b = f64(outs[layer]), f64(o[0])
+        mag = np.abs(f64(v)).max()
+        assert np.max(np.abs(a - b)) <= 2 * (2 ** -7 + 1e-3) * mag
+        assert np.linalg.norm(a - b) <= 1e-2 * np.linalg.norm(b)

@@ -66,6 +66,32 @@ __device__ __forceinline__ int keys_of(const PagedArgs& a, int stream) {
   return kv < most ? kv : static_cast<int>(most);
 }
 
+// Weighted sum of a row's partial results: lane l holds channels 4 l .. + 3.
+struct JoinAcc {
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  float m = -INFINITY, l = 0.f;
+  __device__ __forceinline__ void add(const float2 ml, const float* row,
+                                      int lane) {
+    if (!(ml.y > 0.f)) return;  // saw no key: its O is not read
+    const float4 v = reinterpret_cast<const float4*>(row)[lane];
+    const float mn = fmaxf(m, ml.x);
+    const float w1 = m == -INFINITY ? 0.f : ex2(m - mn);
+    const float w2 = ex2(ml.x - mn);
+    acc.x = fmaf(v.x, w2, acc.x * w1);
+    acc.y = fmaf(v.y, w2, acc.y * w1);
+    acc.z = fmaf(v.z, w2, acc.z * w1);
+    acc.w = fmaf(v.w, w2, acc.w * w1);
+    l = fmaf(ml.y, w2, l * w1);
+    m = mn;
+  }
+  __device__ __forceinline__ void write(__nv_bfloat16* dst, int lane) const {
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+    reinterpret_cast<uint2*>(dst)[lane] =
+        make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv),
+                   pack_bf16x2(acc.z * inv, acc.w * inv));
+  }
+};
+
 // ============================================================== few rows ==
 //
 // The cache's bytes bound this: per key and head 512 bytes are read for at
@@ -461,32 +487,6 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
-// Weighted sum of a row's partial results: lane l holds channels 4 l .. + 3.
-struct JoinAcc {
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  float m = -INFINITY, l = 0.f;
-  __device__ __forceinline__ void add(const float2 ml, const float* row,
-                                      int lane) {
-    if (!(ml.y > 0.f)) return;  // saw no key: its O is not read
-    const float4 v = reinterpret_cast<const float4*>(row)[lane];
-    const float mn = fmaxf(m, ml.x);
-    const float w1 = m == -INFINITY ? 0.f : ex2(m - mn);
-    const float w2 = ex2(ml.x - mn);
-    acc.x = fmaf(v.x, w2, acc.x * w1);
-    acc.y = fmaf(v.y, w2, acc.y * w1);
-    acc.z = fmaf(v.z, w2, acc.z * w1);
-    acc.w = fmaf(v.w, w2, acc.w * w1);
-    l = fmaf(ml.y, w2, l * w1);
-    m = mn;
-  }
-  __device__ __forceinline__ void write(__nv_bfloat16* dst, int lane) const {
-    const float inv = l > 0.f ? 1.f / l : 0.f;
-    reinterpret_cast<uint2*>(dst)[lane] =
-        make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv),
-                   pack_bf16x2(acc.z * inv, acc.w * inv));
-  }
-};
-
 // One warp per (stream, key head, row) whose item several CTAs shared.
 __global__ void __launch_bounds__(128)
     paged_few_join(const __grid_constant__ PagedArgs args) {
@@ -528,6 +528,551 @@ __global__ void __launch_bounds__(128)
   }
 }
 }  // namespace few
+
+// ============================================================= row tiles ==
+//
+// The two-tile pipeline of attn_fwd_kernel (same warp roles, rings, tensor
+// memory and softmax) fed from pages: a 128-key block is 2 to 8 TMA boxes
+// per 64-channel half, one lane of the producer warp per box, the block
+// table entry of the next block fetched while this one loads.  One
+// persistent CTA per SM walks units u = blockIdx.x, + gridDim.x, ... of the
+// plan's list: (256 rows of a stream, head, range of its key blocks), tiles
+// fastest so that neighbours read the same keys at the same time, streams by
+// falling length.  A unit whose rows fit one tile runs that tile alone.
+// Output rows are staged in the tile's own Q buffer (free once the unit's
+// last P V is done) and stored 512 contiguous bytes a warp instruction with
+// a row check, since a stream's last tile ends inside the next stream's rows
+// (a TMA store would overwrite them).  A unit with a part of its keys writes
+// fp32 partial results instead, joined by paged_tile_join.
+namespace tile {
+enum : int {
+  QFULL = 0,
+  KFULL = 1,
+  KEMPTY = KFULL + NSK,
+  VFULL = KEMPTY + NSK,
+  VEMPTY = VFULL + NSV,
+  SFULL = VEMPTY + NSV,    // per tile
+  PREADY = SFULL + QT,     // per tile: 4 warps stored P
+  OFINAL = PREADY + QT,    // per tile: a unit's last P V done
+  TFREE = OFINAL + QT,     // per tile: O read and Q buffer free (4 warps)
+  DRAIN = TFREE + QT,
+  NBAR
+};
+
+struct Unit {
+  int stream, head;
+  int q0;            // packed row of the tile pair's first row
+  int rows;          // its rows, at most 256
+  int a0;            // their first position
+  int kv, chunk, window;
+  int lo, hi;        // keys that any of the rows sees
+  int kb0, nblk;     // key blocks of the unit's range (may be none)
+  int slot;          // partial-result slot, -1: the keys in full
+};
+
+__device__ __forceinline__ Unit unit_at(const PagedArgs& a, int u) {
+  Unit t;
+  const int32_t* e = find_entry(a.c.work, pg::E_BASE, 1, u);
+  t.stream = __ldg(e + pg::E_STREAM);
+  const int tiles = __ldg(e + pg::E_COUNT);
+  const int ns = __ldg(e + pg::E_SPLIT);
+  const int local = u - __ldg(e + pg::E_BASE);
+  const int rest = local / tiles;
+  const int tx = tiles - 1 - (local - rest * tiles);  // longest keys first
+  t.head = rest / ns;
+  const int split = rest - t.head * ns;
+  t.slot = ns > 1 ? __ldg(e + pg::E_SLOT) + local : -1;
+  const int ql = __ldg(a.c.q_lens + t.stream);
+  t.kv = keys_of(a, t.stream);
+  const int4 cfg = __ldg(reinterpret_cast<const int4*>(a.c.streams) + t.stream);
+  t.chunk = cfg.z;
+  t.window = cfg.w;
+  t.q0 = __ldg(a.c.q_start + t.stream) + tx * pg::kTileRows;
+  t.rows = min(ql - tx * pg::kTileRows, pg::kTileRows);
+  t.a0 = t.kv - ql + tx * pg::kTileRows;
+  t.lo = pg::key_lo(max(t.a0, 0), t.chunk, t.window);
+  t.hi = pg::key_hi(t.a0 + t.rows - 1, t.chunk, t.kv);
+  const int b0 = t.lo / BN;
+  const int nb = max((t.hi + BN - 1) / BN - b0, 0);
+  t.kb0 = b0 + split * nb / ns;
+  t.nblk = t.rows > 0 ? b0 + (split + 1) * nb / ns - t.kb0 : 0;
+  return t;
+}
+
+__global__ void __launch_bounds__(wan::kThreads, 1)
+    paged_tile_kernel(const __grid_constant__ CUtensorMap tm_q,
+                      const __grid_constant__ CUtensorMap tm_k,
+                      const __grid_constant__ CUtensorMap tm_v,
+                      const __grid_constant__ PagedArgs args) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t bar[NBAR];
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_abort;
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int units = __ldg(args.c.work + pg::H_MODE) == pg::kModeTile
+                        ? __ldg(args.c.work + pg::H_TOTAL)
+                        : 0;
+  if (static_cast<int>(blockIdx.x) >= units) return;
+  volatile int* abort_flag = &s_abort;
+  int* status = &g_wan_status;
+  const uint32_t raw = smem_u32(smem_raw);
+  uint8_t* sm = smem_raw + (((raw + 1023u) & ~1023u) - raw);
+  uint8_t* sQ = sm;
+  uint8_t* sK = sm + QT * TILE;
+  uint8_t* sV = sK + NSK * TILE;
+  if (threadIdx.x == 0) {
+    s_abort = 0;
+    mbar_init(&bar[QFULL], 1);
+    for (int i = 0; i < NSK; ++i) {
+      mbar_init(&bar[KFULL + i], 1);
+      mbar_init(&bar[KEMPTY + i], 1);
+    }
+    for (int i = 0; i < NSV; ++i) {
+      mbar_init(&bar[VFULL + i], 1);
+      mbar_init(&bar[VEMPTY + i], 1);
+    }
+    for (int t = 0; t < QT; ++t) {
+      mbar_init(&bar[SFULL + t], 1);
+      mbar_init(&bar[PREADY + t], 4);
+      mbar_init(&bar[OFINAL + t], 1);
+      mbar_init(&bar[TFREE + t], 4);
+    }
+    mbar_init(&bar[DRAIN], 1);
+    fence_mbar_init();
+  }
+  if (warp == 9) tmem_alloc(&s_tmem, TMEM_COLS);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s_tmem;
+
+  if (warp >= 8) {
+    setmaxnreg_dec();
+    if (warp == 8) {
+      // ---------------------------------------------------- TMA producer --
+      const bool leader = elect_one();
+      if (leader) {
+        prefetch_tmap(&tm_q);
+        prefetch_tmap(&tm_k);
+        prefetch_tmap(&tm_v);
+      }
+      const int boxes = BN >> args.box_shift;
+      const uint32_t box_bytes = 128u << args.box_shift;
+      const int in_mask = (1 << args.page_shift) - 1;
+      const int row0 = lane << args.box_shift;  // this lane's box
+      bool ok = true;
+      int nq = 0, nq1 = 0, nk = 0, nv = 0;  // units, with a 2nd tile; blocks
+      for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
+        const Unit c = unit_at(args, u);
+        if (c.nblk == 0) continue;
+        const bool two = c.rows > BM;
+        int64_t pos = static_cast<int64_t>(c.kb0) * BN + row0;
+        int page = lane < boxes ? page_of(args, c.stream, pos) : 0;
+        if (nq > 0)
+          ok = wait_warp(&bar[TFREE + 0], (nq - 1) & 1, abort_flag, status);
+        if (ok && two && nq1 > 0)
+          ok = wait_warp(&bar[TFREE + 1], (nq1 - 1) & 1, abort_flag, status);
+        if (!ok) break;
+        if (leader) {
+          mbar_expect_tx(&bar[QFULL], two ? QT * TILE : TILE);
+          for (int t = 0; t < (two ? QT : 1); ++t) {
+            tma_load_4d(sQ + t * TILE, &tm_q, &bar[QFULL], 0, c.head,
+                        c.q0 + t * BM, 0);
+            tma_load_4d(sQ + t * TILE + HALF, &tm_q, &bar[QFULL], 64, c.head,
+                        c.q0 + t * BM, 0);
+          }
+        }
+        ++nq;
+        nq1 += two;
+        const int kvhead = c.head / args.group;
+        for (int j = 0; j < c.nblk && ok; ++j) {
+          const int g = nk;
+          const int in_page = static_cast<int>(pos) & in_mask;
+          const int sk = g % NSK, uk = g / NSK;
+          if (uk > 0)
+            ok = wait_warp(&bar[KEMPTY + sk], (uk - 1) & 1, abort_flag, status);
+          if (!ok) break;
+          if (leader) mbar_expect_tx(&bar[KFULL + sk], TILE);
+          __syncwarp();
+          if (lane < boxes) {
+            uint8_t* dst = sK + sk * TILE + lane * box_bytes;
+            tma_load_4d(dst, &tm_k, &bar[KFULL + sk], 0, in_page, kvhead, page);
+            tma_load_4d(dst + HALF, &tm_k, &bar[KFULL + sk], 64, in_page,
+                        kvhead, page);
+          }
+          ++nk;
+          const int sv = g % NSV, uv = g / NSV;
+          if (uv > 0)
+            ok = wait_warp(&bar[VEMPTY + sv], (uv - 1) & 1, abort_flag, status);
+          if (!ok) break;
+          if (leader) mbar_expect_tx(&bar[VFULL + sv], TILE);
+          __syncwarp();
+          if (lane < boxes) {
+            uint8_t* dst = sV + sv * TILE + lane * box_bytes;
+            tma_load_4d(dst, &tm_v, &bar[VFULL + sv], 0, in_page, kvhead, page);
+            tma_load_4d(dst + HALF, &tm_v, &bar[VFULL + sv], 64, in_page,
+                        kvhead, page);
+            pos += BN;
+            if (j + 1 < c.nblk) page = page_of(args, c.stream, pos);
+          }
+          ++nv;
+          __syncwarp();
+        }
+      }
+      if (*abort_flag) {
+        // copies already issued land before the CTA leaves
+        if (nq > 0) wait_warp_drain(&bar[QFULL], (nq - 1) & 1, status);
+        for (int g = (nk > NSK ? nk - NSK : 0); g < nk; ++g)
+          wait_warp_drain(&bar[KFULL + g % NSK], (g / NSK) & 1, status);
+        for (int g = (nv > NSV ? nv - NSV : 0); g < nv; ++g)
+          wait_warp_drain(&bar[VFULL + g % NSV], (g / NSV) & 1, status);
+      }
+    } else if (warp == 9) {
+      // ------------------------------------------------------ MMA issuer --
+      const uint64_t dq = sdesc_sw128(smem_u32(sQ), 16, 1024);
+      const uint64_t dk = sdesc_sw128(smem_u32(sK), 16, 1024);
+      const uint64_t dv = sdesc_sw128(smem_u32(sV), HALF, 1024);
+      const bool leader = elect_one();
+      auto issue_s = [&](int t, int g) {
+        const uint64_t a0 = dq + ((t * TILE) >> 4);
+        const uint64_t b0 = dk + (((g % NSK) * TILE) >> 4);
+        const uint32_t d = tmem + t * 128;
+        if (leader) {
+#pragma unroll
+          for (int k = 0; k < HD / 16; ++k) {
+            const uint32_t off = ((k >> 2) * HALF + (k & 3) * 32) >> 4;
+            umma_ss(d, a0 + off, b0 + off, IDESC_S, k > 0 ? 1u : 0u);
+          }
+          umma_commit(&bar[SFULL + t]);
+        }
+        __syncwarp();
+      };
+      auto commit = [&](uint64_t* b) {
+        if (leader) umma_commit(b);
+        __syncwarp();
+      };
+      // Waits for V of block g and clears the rows that no row of the unit
+      // sees (before its window, behind its last key): they may hold
+      // anything, and 0 * NaN is not 0.
+      auto ready_v = [&](int g, int kb, const Unit& c) -> bool {
+        if (!wait_warp(&bar[VFULL + g % NSV], (g / NSV) & 1, abort_flag,
+                       status))
+          return false;
+        const int first = c.lo - kb * BN, last = c.hi - kb * BN;
+        if (first > 0 || last < BN) {
+          uint8_t* vt = sV + (g % NSV) * TILE;
+          for (int idx = lane; idx < BN * 16; idx += 32) {
+            const int r = idx >> 4, ch = idx & 15;
+            if (r < first || r >= last)
+              *reinterpret_cast<uint4*>(vt + (ch >> 3) * HALF + r * 128 +
+                                        ((ch & 7) << 4)) =
+                  make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
+        return true;
+      };
+      // O_t += P_t V of ring block g; gt: tile t's own count of blocks, jl:
+      // the block's place in the unit, nt: the tile's units before this one.
+      auto pv = [&](int t, int g, int gt, int jl, int nt) -> bool {
+        if (jl == 0 && nt > 0 &&
+            !wait_warp(&bar[TFREE + t], (nt - 1) & 1, abort_flag, status))
+          return false;
+        if (!wait_warp(&bar[PREADY + t], gt & 1, abort_flag, status))
+          return false;
+        tc_fence_after();
+        const uint64_t b0 = dv + (((g % NSV) * TILE) >> 4);
+        if (leader) {
+#pragma unroll
+          for (int k = 0; k < BN / 16; ++k)
+            umma_ts(tmem + TM_O + t * 128, tmem + t * 128 + k * 8,
+                    b0 + ((k * 2048) >> 4), IDESC_PV,
+                    (jl > 0 || k > 0) ? 1u : 0u);
+        }
+        __syncwarp();
+        return true;
+      };
+      bool ok = true;
+      int g0 = 0, h0 = 0;  // blocks of earlier units: all, with a 2nd tile
+      int n0 = 0, n1 = 0;  // units before this one, with a 2nd tile
+      for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
+        const Unit c = unit_at(args, u);
+        if (c.nblk == 0) continue;
+        const bool two = c.rows > BM;
+        ok = wait_warp(&bar[QFULL], n0 & 1, abort_flag, status);
+        for (int j = 0; j < c.nblk && ok; ++j) {
+          const int g = g0 + j;
+          if (j > 0) {
+            ok = ready_v(g - 1, c.kb0 + j - 1, c) &&
+                 pv(0, g - 1, g - 1, j - 1, n0);
+            if (!ok) break;
+          }
+          ok = wait_warp(&bar[KFULL + g % NSK], (g / NSK) & 1, abort_flag,
+                         status);
+          if (!ok) break;
+          tc_fence_after();
+          issue_s(0, g);
+          if (j > 0) {
+            if (two) {
+              ok = pv(1, g - 1, h0 + j - 1, j - 1, n1);
+              if (!ok) break;
+            }
+            commit(&bar[VEMPTY + (g - 1) % NSV]);
+          }
+          if (two) issue_s(1, g);
+          commit(&bar[KEMPTY + g % NSK]);
+        }
+        if (ok) {
+          const int jl = c.nblk - 1, g = g0 + jl;
+          ok = ready_v(g, c.kb0 + jl, c) && pv(0, g, g, jl, n0);
+          if (ok) {
+            commit(&bar[OFINAL + 0]);
+            if (two) {
+              ok = pv(1, g, h0 + jl, jl, n1);
+              if (ok) commit(&bar[OFINAL + 1]);
+            }
+          }
+          if (ok) commit(&bar[VEMPTY + g % NSV]);
+        }
+        g0 += c.nblk;
+        ++n0;
+        if (two) {
+          h0 += c.nblk;
+          ++n1;
+        }
+      }
+      commit(&bar[DRAIN]);
+      wait_warp_drain(&bar[DRAIN], 0, status);
+    }
+  } else {
+    // ---------------------------------------------------------- softmax --
+    setmaxnreg_inc();
+    const int t = warp >> 2;
+    const int r = threadIdx.x & 127;  // row in the tile == TMEM lane
+    const uint32_t lane_base =
+        tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    const uint32_t s_col = lane_base + t * 128;
+    const uint32_t o_col = lane_base + TM_O + t * 128;
+    const float c2 = args.scale_log2;
+    bool ok = true;
+    int gt = 0, nt = 0;  // this tile's blocks and units so far
+    for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
+      int kb0, nblk, row_lo = 0, row_hi = INT32_MAX;
+      {
+        const Unit c = unit_at(args, u);
+        kb0 = c.kb0;
+        nblk = c.nblk;
+        if (t * BM + r < c.rows) {
+          const int a = c.a0 + t * BM + r;
+          row_lo = pg::key_lo(max(a, 0), c.chunk, c.window);
+          row_hi = pg::key_hi(a, c.chunk, c.kv);
+        }
+        // rows behind the tile's last take part unmasked, never written
+        if (t * BM >= c.rows) continue;  // a unit of one tile
+      }
+      float m_run = -INFINITY;
+      float l_run = 0.f;
+      for (int j = 0; j < nblk; ++j) {
+        ok = wait_warp(&bar[SFULL + t], (gt + j) & 1, abort_flag, status);
+        if (!ok) break;
+        tc_fence_after();
+        float s[BN];
+        tmem_ld128(s_col, s);
+        tmem_ld_wait128(s);
+        const int key0 = (kb0 + j) * BN;
+        const int lim_lo = row_lo - key0, lim_hi = row_hi - key0;
+        const bool masked =
+            __any_sync(0xffffffffu, lim_hi < BN || lim_lo > 0);
+        if (masked) {
+#pragma unroll
+          for (int c = 0; c < BN; ++c)
+            if (c >= lim_hi || c < lim_lo) s[c] = -INFINITY;
+        }
+        const float mx = (masked ? rowmax_masked<BN>(s) : rowmax<BN>(s)) * c2;
+        if (j == 0) {
+          m_run = mx;
+        } else {
+          // S_t(j) complete implies P V_t(j - 1) complete, so O holds
+          // exactly the earlier blocks
+          const bool need = mx > m_run + RESCALE_LOG2;
+          if (__any_sync(0xffffffffu, need)) {
+            // (a row without keys so far keeps m = -inf and factor 1)
+            const float alpha = need ? ex2(m_run - mx) : 1.f;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              float o[32];
+              tmem_ld32(o_col + c * 32, o);
+              tmem_ld_wait32(o);
+#pragma unroll
+              for (int e = 0; e < 32; e += 2) {
+                const float2 v =
+                    ffma2(make_float2(o[e], o[e + 1]),
+                          make_float2(alpha, alpha), make_float2(0.f, 0.f));
+                o[e] = v.x;
+                o[e + 1] = v.y;
+              }
+              tmem_st32(o_col + c * 32, o);
+            }
+            l_run *= alpha;
+            if (need) m_run = mx;
+          }
+        }
+        float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f),
+                         make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        if (masked)
+          exp_store_chunks<false>(s, c2, m_run == -INFINITY ? 0.f : m_run,
+                                  s_col, acc, 0, 4);
+        else
+          exp_store_chunks<true>(s, c2, m_run, s_col, acc, 0, 4);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar[PREADY + t]);
+        const float2 tsum = fadd2(fadd2(acc[0], acc[1]), fadd2(acc[2], acc[3]));
+        l_run += tsum.x + tsum.y;
+      }
+      if (!ok) break;
+      gt += nblk;
+      if (nblk > 0) {
+        ok = wait_warp(&bar[OFINAL + t], nt & 1, abort_flag, status);
+        if (!ok) break;
+        tc_fence_after();
+      }
+      // Coordinates again instead of holding them through the key loop.
+      int u_e = u;
+      asm volatile("" : "+r"(u_e));
+      const Unit ce = unit_at(args, u_e);
+      const int wrow0 = (warp & 3) * 32;  // this warp's rows of the tile
+      const int live = min(ce.rows - t * BM - wrow0,
+                           args.c.token_cap - ce.q0 - t * BM - wrow0);
+      uint8_t* stg = sQ + t * TILE;
+      // A row's 16 pieces of 16 bytes go to its place in the Q buffer
+      // (swizzled by row, as TMA leaves Q), then half-warps store whole
+      // 256-byte rows.
+      auto stage = [&](int piece, uint4 v) {
+        *reinterpret_cast<uint4*>(stg + (piece >> 3) * HALF + r * 128 +
+                                  (((piece & 7) ^ (r & 7)) << 4)) = v;
+      };
+      auto flush = [&](uint8_t* dst, int64_t row_bytes) {
+        __syncwarp();
+#pragma unroll 4
+        for (int i = 0; i < 16; ++i) {
+          const int rr = 2 * i + (lane >> 4), piece = lane & 15;
+          const int row = wrow0 + rr;
+          const uint4 v = *reinterpret_cast<const uint4*>(
+              stg + (piece >> 3) * HALF + row * 128 +
+              (((piece & 7) ^ (row & 7)) << 4));
+          if (rr < live)
+            *reinterpret_cast<uint4*>(dst + rr * row_bytes + piece * 16) = v;
+        }
+        __syncwarp();
+      };
+      if (ce.slot >= 0) {
+        const int64_t prow =
+            static_cast<int64_t>(ce.slot) * pg::kTileRows + t * BM + wrow0;
+        if (lane < live)
+          args.part_ml[prow + lane] = make_float2(m_run, l_run);
+        if (nblk > 0) {
+#pragma unroll 1
+          for (int hc = 0; hc < 2; ++hc) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              float o[32];
+              tmem_ld32(o_col + hc * 64 + c * 32, o);
+              tmem_ld_wait32(o);
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                stage(c * 8 + e,
+                      make_uint4(__float_as_uint(o[4 * e]),
+                                 __float_as_uint(o[4 * e + 1]),
+                                 __float_as_uint(o[4 * e + 2]),
+                                 __float_as_uint(o[4 * e + 3])));
+            }
+            flush(reinterpret_cast<uint8_t*>(args.part_o + prow * HD +
+                                             hc * 64),
+                  HD * 4);
+          }
+        }
+      } else {
+        const int64_t row =
+            (static_cast<int64_t>(ce.q0) + t * BM + wrow0) * args.c.heads +
+            ce.head;
+        uint8_t* dst = reinterpret_cast<uint8_t*>(args.o + row * HD);
+        const int64_t row_bytes = static_cast<int64_t>(args.c.heads) * HD * 2;
+        if (nblk == 0) {
+          // no row sees a key (the Q buffer is not this unit's: no staging)
+          for (int i = lane >> 4; i < live; i += 2)
+            *reinterpret_cast<uint4*>(dst + i * row_bytes + (lane & 15) * 16) =
+                make_uint4(0, 0, 0, 0);
+          continue;
+        }
+        const float inv = l_run > 0.f ? 1.0f / l_run : 0.f;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          float o[32];
+          tmem_ld32(o_col + c * 32, o);
+          tmem_ld_wait32(o);
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            stage(c * 4 + e,
+                  make_uint4(
+                      pack_bf16x2(o[8 * e] * inv, o[8 * e + 1] * inv),
+                      pack_bf16x2(o[8 * e + 2] * inv, o[8 * e + 3] * inv),
+                      pack_bf16x2(o[8 * e + 4] * inv, o[8 * e + 5] * inv),
+                      pack_bf16x2(o[8 * e + 6] * inv, o[8 * e + 7] * inv)));
+        }
+        flush(dst, row_bytes);
+      }
+      if (nblk > 0) {
+        // O is read and the staging rows too: the next unit's first P V and
+        // Q load may overwrite them
+        ++nt;
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar[TFREE + t]);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc(tmem, TMEM_COLS);
+  }
+}
+
+// One warp per (row, head) of the streams whose keys were split.
+__global__ void __launch_bounds__(128)
+    paged_tile_join(const __grid_constant__ PagedArgs args) {
+  const int32_t* work = args.c.work;
+  if (work[pg::H_MODE] != pg::kModeTile) return;
+  const int total = work[pg::H_ROWS];
+  const int lane = threadIdx.x & 31;
+  const int64_t warps = static_cast<int64_t>(gridDim.x) * 4;
+  const int heads = args.c.heads;
+  for (int64_t it = blockIdx.x * 4ll + (threadIdx.x >> 5); it < total;
+       it += warps) {
+    const int32_t* e = find_entry(work, pg::E_ROW, 1, it);
+    const int stream = e[pg::E_STREAM];
+    const int tiles = e[pg::E_COUNT], ns = e[pg::E_SPLIT];
+    const int local = static_cast<int>(it) - e[pg::E_ROW];
+    const int i = local / heads, head = local - i * heads;
+    const int64_t row = static_cast<int64_t>(args.c.q_start[stream]) + i;
+    if (row >= args.c.token_cap) continue;
+    const int tx = tiles - 1 - i / pg::kTileRows;
+    JoinAcc acc;
+    for (int s = 0; s < ns; ++s) {
+      const int64_t slot = e[pg::E_SLOT] + (head * ns + s) * tiles + tx;
+      const int64_t prow = slot * pg::kTileRows + i % pg::kTileRows;
+      acc.add(args.part_ml[prow], args.part_o + prow * HD, lane);
+    }
+    acc.write(args.o + (row * heads + head) * HD, lane);
+  }
+}
+}  // namespace tile
 
 int paged_box_rows(const wan_paged_t* c) {
   return c->page_size < 64 ? c->page_size : 64;
@@ -585,6 +1130,43 @@ int launch_few(const CUtensorMap& mk, const CUtensorMap& mv,
   return cudaGetLastError() == cudaSuccess ? WAN_OK : WAN_ECUDA;
 }
 
+int launch_tile(const CUtensorMap& mk, const CUtensorMap& mv,
+                const PagedArgs& a, int sms, cudaStream_t s) {
+  static std::mutex mu;
+  static int state[64];  // 0 unknown, 1 ready, 2 unusable
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64)
+    return WAN_ECUDA;
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    if (state[dev] == 0) {
+      // setmaxnreg draws on the registers the CTA was launched with
+      cudaFuncAttributes fa;
+      if (cudaFuncGetAttributes(&fa, tile::paged_tile_kernel) != cudaSuccess)
+        return WAN_ECUDA;
+      if (fa.numRegs * kThreads <
+          8 * 32 * kSoftmaxRegs + 4 * 32 * kOtherRegs) {
+        state[dev] = 2;
+      } else if (cudaFuncSetAttribute(
+                     tile::paged_tile_kernel,
+                     cudaFuncAttributeMaxDynamicSharedMemorySize,
+                     SMEM_DYN) != cudaSuccess) {
+        return WAN_ECUDA;
+      } else {
+        state[dev] = 1;
+      }
+    }
+    if (state[dev] != 1) return WAN_EUNSUPPORTED;
+  }
+  CUtensorMap mq;
+  const int st = make_map_bf16(&mq, a.q, 1, a.c.token_cap, a.c.heads, BM);
+  if (st != WAN_OK) return st;
+  tile::paged_tile_kernel<<<sms, kThreads, SMEM_DYN, s>>>(mq, mk, mv, a);
+  if (cudaGetLastError() != cudaSuccess) return WAN_ECUDA;
+  tile::paged_tile_join<<<8 * sms, 128, 0, s>>>(a);
+  return cudaGetLastError() == cudaSuccess ? WAN_OK : WAN_ECUDA;
+}
+
 }  // namespace
 }  // namespace wan
 
@@ -633,8 +1215,8 @@ int wan_paged_attn(const wan_paged_t* c, const void* q, const void* k_pages,
   a.group = c->heads / c->kv_heads;
   a.page_shift = paged_log2(c->page_size);
   a.box_shift = paged_log2(box);
-  if (!paged::few_mode(c)) return WAN_EUNSUPPORTED;
-  return launch_few(mk, mv, a, sms, as_stream(s));
+  return paged::few_mode(c) ? launch_few(mk, mv, a, sms, as_stream(s))
+                            : launch_tile(mk, mv, a, sms, as_stream(s));
 }
 
 }  // extern "C"
