@@ -24,6 +24,9 @@ import torch
 from . import wan
 
 
+_SCALE = 1.0 / math.sqrt(128)
+
+
 def _pad4(n):
     """int32 counts padded to whole 16-byte pieces."""
     return -(-int(n) // 4) * 4
@@ -100,7 +103,13 @@ class PagedCache:
          self._work) = parts(buf, counts)
         self.tokens = tokens.view(self.token_cap, 4)
         self.tokens.fill_(-1)
-        self._workspace = None
+        self._index = streams.get_device()
+        self._desc = None
+        self._workspace = self._workspace_for = None
+        self._q_shape = torch.Size((self.token_cap, self.heads, 128))
+        self._kv_shape = torch.Size((self.token_cap, self.kv_heads, 128))
+        self._pool_shape = torch.Size((self.n_pages, self.kv_heads,
+                                       self.page_size, 128))
         self.reset()
 
     def reset(self):
@@ -113,36 +122,41 @@ class PagedCache:
 
     def new_pools(self, layers=None):
         """Zeroed K and V pools of one layer, or [layers, ...] of several."""
-        shape = (self.n_pages, self.kv_heads, self.page_size, 128)
+        shape = tuple(self._pool_shape)
         if layers is not None:
             shape = (int(layers),) + shape
         return (torch.zeros(shape, dtype=torch.bfloat16, device=self.device),
                 torch.zeros(shape, dtype=torch.bfloat16, device=self.device))
 
     def descriptor(self):
-        """The wan_paged_t of the cache."""
-        return wan.PagedDesc(
-            self.n_streams, self.max_pages, self.n_pages, self.page_size,
-            self.token_cap, self.max_new, self.heads, self.kv_heads,
-            self.grid, *(t.data_ptr() for t in (
-                self.streams, self.kv_lens, self.first_pages,
-                self.block_table, self.free_ring, self.ring_state,
-                self.q_start, self.q_lens, self.status, self.tokens,
-                self._work)))
+        """The wan_paged_t of the cache (its arrays stay where they are for
+        the cache's life, so it is built once)."""
+        d = self._desc
+        if d is None:
+            d = self._desc = wan.PagedDesc(
+                self.n_streams, self.max_pages, self.n_pages, self.page_size,
+                self.token_cap, self.max_new, self.heads, self.kv_heads,
+                self.grid, *(t.data_ptr() for t in (
+                    self.streams, self.kv_lens, self.first_pages,
+                    self.block_table, self.free_ring, self.ring_state,
+                    self.q_start, self.q_lens, self.status, self.tokens,
+                    self._work)))
+        d.max_new = self.max_new
+        return d
 
-    def _rows(self, t, heads, name):
-        if t.dtype != torch.bfloat16 or not t.is_contiguous():
-            raise ValueError("%s must be a contiguous bf16 tensor" % name)
-        wan._shape_is(t, (self.token_cap, heads, 128), name)
-
-    def _pool(self, t, name):
-        if t.dtype != torch.bfloat16 or not t.is_contiguous():
-            raise ValueError("%s must be a contiguous bf16 tensor" % name)
-        wan._shape_is(t, (self.n_pages, self.kv_heads, self.page_size, 128),
-                      name)
+    def _check(self, shape, *named):
+        """Contiguous bf16 tensors of one shape on the cache's device."""
+        for name, t in named:
+            if t.dtype != torch.bfloat16 or not t.is_contiguous():
+                raise ValueError("%s must be a contiguous bf16 tensor" % name)
+            if t.shape != shape:
+                wan._shape_is(t, shape, name)
+        self._here(*named)
 
     def _here(self, *named):
-        wan._on_cuda(("streams", self.streams), *named)
+        for name, t in named:
+            if t.get_device() != self._index:
+                wan._on_cuda(("streams", self.streams), (name, t))
 
     def plan(self, new_lens, stream=None):
         """Plans a step: new_lens int32 CUDA tensor [R], > 0 new tokens of
@@ -159,20 +173,16 @@ class PagedCache:
         place), k into its slots of k_pages; v into v_pages
         (wan_paged_write)."""
         q_out = q if q_out is None else q_out
-        self._rows(q, self.heads, "q")
-        self._rows(q_out, self.heads, "q_out")
-        self._rows(k, self.kv_heads, "k")
-        self._rows(v, self.kv_heads, "v")
-        self._pool(k_pages, "k_pages")
-        self._pool(v_pages, "v_pages")
+        self._check(self._q_shape, ("q", q), ("q_out", q_out))
+        self._check(self._kv_shape, ("k", k), ("v", v))
+        self._check(self._pool_shape, ("k_pages", k_pages),
+                    ("v_pages", v_pages))
         wan._f32_n(wq, self.heads * 128, "wq")
         wan._f32_n(wk, self.kv_heads * 128, "wk")
         if table is None:
             raise ValueError("write needs a RoPE table")
         wan._check_table(table, self.grid, 128)
-        self._here(("q", q), ("q_out", q_out), ("k", k), ("v", v),
-                   ("wq", wq), ("wk", wk), ("table", table),
-                   ("k_pages", k_pages), ("v_pages", v_pages))
+        self._here(("wq", wq), ("wk", wk), ("table", table))
         wan.paged_write(self.descriptor(), q, q_out, k, v, wq, wk, k_pages,
                         v_pages, table, eps, stream=stream)
 
@@ -180,27 +190,26 @@ class PagedCache:
         """The attention's scratch of this cache, allocated on first use.
         Calls that overlap on the device need one each (``attn``'s
         workspace argument)."""
-        need = wan.paged_workspace_bytes(self.descriptor(), self.device)
-        if self._workspace is None or self._workspace.numel() < need:
-            self._workspace = torch.empty(need, dtype=torch.uint8,
-                                          device=self.device)
+        if self._workspace is None or self._workspace_for != self.max_new:
+            need = wan.paged_workspace_bytes(self.descriptor(), self.device)
+            if self._workspace is None or self._workspace.numel() < need:
+                self._workspace = torch.empty(need, dtype=torch.uint8,
+                                              device=self.device)
+            self._workspace_for = self.max_new
         return self._workspace
 
-    def attn(self, q, k_pages, v_pages, o, softmax_scale=None, stream=None,
+    def attn(self, q, k_pages, v_pages, o, softmax_scale=_SCALE, stream=None,
              workspace=None):
         """o = softmax(q K^T scale) V over the pages for the planned rows
         (wan_paged_attn)."""
-        self._rows(q, self.heads, "q")
-        self._rows(o, self.heads, "o")
-        self._pool(k_pages, "k_pages")
-        self._pool(v_pages, "v_pages")
-        self._here(("q", q), ("o", o), ("k_pages", k_pages),
-                   ("v_pages", v_pages), ("workspace", workspace))
-        if softmax_scale is None:
-            softmax_scale = 1.0 / math.sqrt(128)
+        self._check(self._q_shape, ("q", q), ("o", o))
+        self._check(self._pool_shape, ("k_pages", k_pages),
+                    ("v_pages", v_pages))
         if workspace is None:
             workspace = self.workspace()
-        if not workspace.is_contiguous():
-            raise ValueError("workspace must be a contiguous tensor")
+        else:
+            self._here(("workspace", workspace))
+            if not workspace.is_contiguous():
+                raise ValueError("workspace must be a contiguous tensor")
         wan.paged_attn(self.descriptor(), q, k_pages, v_pages, o,
                        softmax_scale, workspace, stream=stream)

@@ -612,35 +612,40 @@ def paged_workspace_bytes(desc, device):
     """Workspace bytes of wan_paged_attn on a device."""
     import torch
     with torch.cuda.device(device):
-        return lib().wan_paged_workspace_bytes(ctypes.byref(desc))
+        return lib().wan_paged_workspace_bytes(desc)
+
+
+def _paged_call(name, t, stream, *args):
+    """One call with t's device current, on stream or its current stream."""
+    import torch
+    index = t.get_device()
+    if torch.cuda.current_device() != index:
+        with torch.cuda.device(index):
+            return _paged_call(name, t, stream, *args)
+    if stream is None:
+        stream = torch.cuda.current_stream()
+    _check(getattr(lib(), name)(*args, stream.cuda_stream), name)
 
 
 def paged_plan(desc, new_lens, stream=None):
-    import torch
-    with torch.cuda.device(new_lens.device):
-        _check(lib().wan_paged_plan(ctypes.byref(desc), _ptr(new_lens),
-                                    _stream(stream)), "wan_paged_plan")
+    _paged_call("wan_paged_plan", new_lens, stream, desc,
+                new_lens.data_ptr())
 
 
 def paged_write(desc, q, q_out, k, v, wq, wk, k_pages, v_pages, table, eps,
                 stream=None):
-    import torch
-    with torch.cuda.device(q.device):
-        _check(lib().wan_paged_write(
-            ctypes.byref(desc), _ptr(q), _ptr(q_out), _ptr(k), _ptr(v),
-            _ptr(wq), _ptr(wk), _ptr(k_pages), _ptr(v_pages), _ptr(table),
-            eps, _stream(stream)), "wan_paged_write")
+    _paged_call("wan_paged_write", q, stream, desc, q.data_ptr(),
+                q_out.data_ptr(), k.data_ptr(), v.data_ptr(), wq.data_ptr(),
+                wk.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
+                table.data_ptr(), eps)
 
 
 def paged_attn(desc, q, k_pages, v_pages, o, softmax_scale, workspace,
                stream=None):
-    import torch
-    with torch.cuda.device(q.device):
-        _check(lib().wan_paged_attn(
-            ctypes.byref(desc), _ptr(q), _ptr(k_pages), _ptr(v_pages),
-            _ptr(o), softmax_scale, _ptr(workspace),
-            workspace.numel() * workspace.element_size(), _stream(stream)),
-            "wan_paged_attn")
+    _paged_call("wan_paged_attn", q, stream, desc, q.data_ptr(),
+                k_pages.data_ptr(), v_pages.data_ptr(), o.data_ptr(),
+                softmax_scale, workspace.data_ptr(),
+                workspace.numel() * workspace.element_size())
 
 
 def attn_pair_resident_clusters():
