@@ -109,12 +109,13 @@ __device__ __forceinline__ int find_stream(const int* incl, int n, int x) {
 constexpr int kUnitCost = 3;
 constexpr int kJoinCost = 2;
 constexpr int kSlotsPerBlock = 50;
+constexpr int kMinStages = 1;  // stages of a CTA on the few-row kernel
 constexpr int kMinRange = 8;  // key blocks of a range
 
 // The attention's work list, by one CTA.  ql and kv are stream threadIdx.x's
 // rows and keys.
-__device__ void build_work(const PlanArgs& a, int ql, int kv, int chunk,
-                           int window, uint64_t* red, int* s_a, int* s_b,
+__device__ void build_work(const PlanArgs& a, int ql, int kv, int q0,
+                           int chunk, int window, uint64_t* red, int* s_a, int* s_b,
                            int* s_c, int64_t* s_cost) {
   const wan_paged_t& c = a.c;
   const int r = threadIdx.x;
@@ -135,12 +136,15 @@ __device__ void build_work(const PlanArgs& a, int ql, int kv, int chunk,
       e[E_STREAM] = r;
       e[E_BASE] = base;
       e[E_COUNT] = n;
+      e[E_STAGE0] = min(lo, kv - 1) / kStage;
+      e[E_KV] = kv;
+      e[E_ROWS] = ql;
+      e[E_Q0] = q0;
     }
     if (r == blockDim.x - 1) {
       const int64_t total = static_cast<int64_t>(base + n) * c.kv_heads;
-      // at least 2 stages a CTA: one stage is a full pipeline latency
-      int64_t ctas = total / 2;
       const int64_t most = static_cast<int64_t>(a.sms) * kFewCtasPerSm;
+      int64_t ctas = total / kMinStages;
       ctas = ctas < 1 ? 1 : ctas > most ? most : ctas;
       work[H_MODE] = kModeFew;
       work[H_ACTIVE] = idx + on;
@@ -400,7 +404,7 @@ __global__ void __launch_bounds__(kPlanThreads)
   // the last CTA has no state to write
   if (rank == ctas - 1) {
     __syncthreads();
-    build_work(a, admit ? rows : 0, kv, cfg.z, cfg.w, red, s_back, s_need,
+    build_work(a, admit ? rows : 0, kv, r ? s_end[r - 1] : 0, cfg.z, cfg.w, red, s_back, s_need,
                s_from, s_cost);
   }
 }

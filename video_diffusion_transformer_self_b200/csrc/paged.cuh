@@ -41,7 +41,27 @@ enum : int {
   E_COUNT = 2,    // kFew: its stages; kTile: its 256-row tiles
   E_SPLIT = 3,    // kTile: key ranges
   E_SLOT = 4,     // kTile: first partial-result slot (nsplit > 1)
-  E_ROW = 5       // kTile: split (row, head) pairs before it
+  E_ROW = 5,      // kTile: split (row, head) pairs before it
+  // kFew: what a CTA needs to start fetching, in one 32-byte read
+  E_STAGE0 = 3,   // first stage
+  E_KV = 4,       // tokens of the stream
+  E_ROWS = 5,     // its new tokens
+  E_Q0 = 6        // their first packed row
+};
+
+// kFew: CTA c of `ctas` takes places [first(c), first(c + 1)) of the line of
+// `total`; the first total % ctas CTAs take one more.
+struct Line {
+  int each, more;
+  __host__ __device__ __forceinline__ Line(int total, int ctas)
+      : each(total / ctas), more(total % ctas) {}
+  __host__ __device__ __forceinline__ int first(int c) const {
+    return c * each + (c < more ? c : more);
+  }
+  __host__ __device__ __forceinline__ int cta_of(int x) const {
+    const int big = more * (each + 1);
+    return x < big ? x / (each + 1) : more + (x - big) / each;
+  }
 };
 
 // First key that the query at position a sees, and one past its last.

@@ -66,23 +66,69 @@ __device__ __forceinline__ int keys_of(const PagedArgs& a, int stream) {
   return kv < most ? kv : static_cast<int>(most);
 }
 
+// Waits until the kernel before this one on the stream has finished (the
+// joins are launched early, while it still runs).
+__device__ __forceinline__ void grid_dependency_wait() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+__device__ __forceinline__ void launch_dependents() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 // Weighted sum of a row's partial results: lane l holds channels 4 l .. + 3.
 struct JoinAcc {
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   float m = -INFINITY, l = 0.f;
-  __device__ __forceinline__ void add(const float2 ml, const float* row,
-                                      int lane) {
-    if (!(ml.y > 0.f)) return;  // saw no key: its O is not read
-    const float4 v = reinterpret_cast<const float4*>(row)[lane];
-    const float mn = fmaxf(m, ml.x);
-    const float w1 = m == -INFINITY ? 0.f : ex2(m - mn);
-    const float w2 = ex2(ml.x - mn);
-    acc.x = fmaf(v.x, w2, acc.x * w1);
-    acc.y = fmaf(v.y, w2, acc.y * w1);
-    acc.z = fmaf(v.z, w2, acc.z * w1);
-    acc.w = fmaf(v.w, w2, acc.w * w1);
-    l = fmaf(ml.y, w2, l * w1);
-    m = mn;
+  // Parts 0 .. n - 1, part k at row_of(k) of the workspace.  32 parts at a
+  // time: their maxima and sums come with one load a lane, their O rows with
+  // batches of independent loads (loads under a condition ran one after the
+  // other: 25 parts took 13 us instead of 4).
+  static constexpr int kBatch = 16;
+  template <typename RowOf>
+  __device__ __forceinline__ void add_all(int n, int lane,
+                                          const PagedArgs& a, RowOf row_of) {
+    for (int k0 = 0; k0 < n; k0 += 32) {
+      float2 ml = make_float2(-INFINITY, 0.f);
+      if (k0 + lane < n) ml = a.part_ml[row_of(k0 + lane)];
+      // a part that saw no key has no O
+      if (!(ml.y > 0.f)) ml = make_float2(-INFINITY, 0.f);
+      float top = ml.x;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1)
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      if (top == -INFINITY) continue;
+      const float mn = fmaxf(m, top);
+      const float w0 = m == -INFINITY ? 0.f : ex2(m - mn);
+      const float w = ml.x == -INFINITY ? 0.f : ex2(ml.x - mn);
+      float sum = ml.y * w;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1)
+        sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      l = fmaf(l, w0, sum);
+      m = mn;
+      acc = make_float4(acc.x * w0, acc.y * w0, acc.z * w0, acc.w * w0);
+      const int cnt = min(n - k0, 32);
+      for (int b = 0; b < cnt; b += kBatch) {
+        // all loads of a batch first (a part without keys is loaded too,
+        // whatever it holds, and dropped)
+        float4 v[kBatch];
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k)
+          v[k] = reinterpret_cast<const float4*>(
+              a.part_o + row_of(k0 + min(b + k, cnt - 1)) * HD)[lane];
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+          const float wk = __shfl_sync(0xffffffffu, w, (b + k) & 31);
+          if (b + k < cnt && wk > 0.f) {
+            acc.x = fmaf(v[k].x, wk, acc.x);
+            acc.y = fmaf(v[k].y, wk, acc.y);
+            acc.z = fmaf(v[k].z, wk, acc.z);
+            acc.w = fmaf(v[k].w, wk, acc.w);
+          }
+        }
+      }
+    }
   }
   __device__ __forceinline__ void write(__nv_bfloat16* dst, int lane) const {
     const float inv = l > 0.f ? 1.f / l : 0.f;
@@ -99,50 +145,73 @@ struct JoinAcc {
 // fast enough and keeps everything in registers.  The step's (stream, key
 // head, 64-key stage) items form one line that is cut into equal parts, one
 // per CTA, so every SM reads the same number of bytes whatever the streams'
-// lengths.  Warp 4 fetches stages (K and V, 32 KB) through a 3-stage TMA
-// ring, 192 KB in flight per SM with two CTAs; warps 0-3 take 16 keys of a
-// stage each, with a softmax state of their own, and are joined when the
-// CTA leaves an item.  An item that several CTAs share is written as
-// partial results (at most two per CTA) and joined by paged_few_join.
+// lengths.  Each of a CTA's four warps takes 16 keys of every stage (4 KB of
+// K and of V, contiguous in their page) through a 3-deep ring of its own,
+// filled with cp.async, so no warp waits for another until the CTA leaves an
+// item and the four softmax states are joined; the ring runs on across
+// items.  Two CTAs per SM keep up to 192 KB in flight.  An item that several
+// CTAs share is written as partial results (at most two per CTA) and joined
+// by paged_few_join.
 namespace few {
-constexpr int kThreads = 160;
-constexpr int kStages = 3;
-constexpr uint32_t kHalf = pg::kStage * 128;   // [64 keys][64 ch] bf16
-constexpr uint32_t kStageBytes = 4 * kHalf;    // K halves, V halves
+constexpr int kWarps = 4;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kDepth = 3;
+constexpr int kKeys = pg::kStage / kWarps;     // keys of a warp's part: 16
+constexpr uint32_t kPart = kKeys * HD * 2;     // its K (or V): 4 KB
+constexpr uint32_t kWarpRing = kDepth * 2 * kPart;
 constexpr int kRows = pg::kFewRows;
 constexpr uint32_t kJoinFloats = kRows * HD + 2 * kRows;
-constexpr uint32_t kSmem =
-    kStages * kStageBytes + 2 * kJoinFloats * 4 + 1024;
+constexpr uint32_t kSmem = kWarps * kWarpRing + 2 * kJoinFloats * 4;
+static_assert(kKeys == 16, "one k-step of P V, and never two pages");
 
 struct Segment {
   int stream, head, kv, ql, q0;  // q0: packed row of the stream's first row
   int stage0, n;                 // stages [stage0, stage0 + n) of 64 keys
   bool whole;                    // the item in full
-  int chunk, window;
 };
 
 // The part of an item that starts at x, up to x1 on the line.
-__device__ __forceinline__ Segment segment_at(const PagedArgs& a, int64_t x,
-                                              int64_t x1) {
+__device__ __forceinline__ Segment segment_at(const PagedArgs& a, int x,
+                                              int x1) {
   Segment s;
-  const int kvh = a.c.kv_heads;
-  const int32_t* e = find_entry(a.c.work, pg::E_BASE, kvh, x);
-  s.stream = __ldg(e + pg::E_STREAM);
-  const int n = __ldg(e + pg::E_COUNT);
-  const int64_t local = x - static_cast<int64_t>(__ldg(e + pg::E_BASE)) * kvh;
-  s.head = static_cast<int>(local / n);
-  const int at = static_cast<int>(local - static_cast<int64_t>(s.head) * n);
-  s.n = static_cast<int>(n - at < x1 - x ? n - at : x1 - x);
+  const int4* e = reinterpret_cast<const int4*>(
+      find_entry(a.c.work, pg::E_BASE, a.c.kv_heads, x));
+  const int4 e0 = __ldg(e), e1 = __ldg(e + 1);
+  s.stream = e0.x;
+  const int n = e0.z;
+  const int local = x - e0.y * a.c.kv_heads;
+  s.head = local / n;
+  const int at = local - s.head * n;
+  s.n = min(n - at, x1 - x);
   s.whole = s.n == n;
-  s.kv = keys_of(a, s.stream);
-  s.ql = __ldg(a.c.q_lens + s.stream);
-  s.q0 = __ldg(a.c.q_start + s.stream);
-  const int4 cfg = __ldg(reinterpret_cast<const int4*>(a.c.streams) + s.stream);
-  s.chunk = cfg.z;
-  s.window = cfg.w;
-  const int lo = pg::key_lo(max(s.kv - s.ql, 0), s.chunk, s.window);
-  s.stage0 = max(min(lo, s.kv - 1), 0) / pg::kStage + at;
+  s.stage0 = e0.w + at;
+  s.kv = e1.x;
+  s.ql = e1.y;
+  s.q0 = e1.z;
   return s;
+}
+
+// 16 bytes global -> shared, zeros instead of the global bytes if !live.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src,
+                                           bool live) {
+  const int n = live ? 16 : 0;
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst),
+               "l"(src), "r"(n)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int kPending>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory");
+}
+
+// Row r, 16-byte chunk c of a warp's 16 rows of 256 bytes: the chunk's low
+// bits are turned by the row, so that the 8 rows of an ldmatrix lie in
+// different banks.
+__device__ __forceinline__ uint32_t swz(int r, int c) {
+  return r * 256 + ((c ^ (r & 7)) << 4);
 }
 
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
@@ -169,102 +238,87 @@ __device__ __forceinline__ void mma16816(float (&d)[4],
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-__global__ void __launch_bounds__(kThreads)
-    paged_few_kernel(const __grid_constant__ CUtensorMap tm_k,
-                     const __grid_constant__ CUtensorMap tm_v,
+__global__ void __launch_bounds__(kThreads, pg::kFewCtasPerSm)
+    paged_few_kernel(const __nv_bfloat16* __restrict__ k_pages,
+                     const __nv_bfloat16* __restrict__ v_pages,
                      const __grid_constant__ PagedArgs args) {
-  extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t full[kStages];
-  __shared__ __align__(8) uint64_t empty[kStages];
-  __shared__ int s_abort;
+  extern __shared__ __align__(128) uint8_t smem_raw[];
   const int32_t* work = args.c.work;
   const int ctas = __ldg(work + pg::H_CTAS);
   const int cta = blockIdx.x;
   if (__ldg(work + pg::H_MODE) != pg::kModeFew || cta >= ctas ||
       __ldg(work + pg::H_ACTIVE) < 1)
     return;
-  const int64_t total = __ldg(work + pg::H_TOTAL);
-  const int64_t x0 = cta * total / ctas, x1 = (cta + 1) * total / ctas;
-
-  const uint32_t raw = smem_u32(smem_raw);
-  const uint32_t sm = (raw + 1023u) & ~1023u;
-  float* join = reinterpret_cast<float*>(smem_raw + (sm - raw) +
-                                         kStages * kStageBytes);
+  const pg::Line line(__ldg(work + pg::H_TOTAL), ctas);
+  const int x0 = line.first(cta), x1 = line.first(cta + 1);
+  launch_dependents();
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  volatile int* abort_flag = &s_abort;
-  int* status = &g_wan_status;
-  if (threadIdx.x == 0) {
-    s_abort = 0;
-    for (int i = 0; i < kStages; ++i) {
-      mbar_init(&full[i], 1);
-      mbar_init(&empty[i], 4);
-    }
-    fence_mbar_init();
-  }
-  __syncthreads();
+  float* join = reinterpret_cast<float*>(smem_raw + kWarps * kWarpRing);
+  const uint32_t ring = smem_u32(smem_raw) + warp * kWarpRing;
+  const float c2 = args.scale_log2;
+  const int heads = args.c.heads;
+  const int page_mask = (1 << args.page_shift) - 1;
+  const int64_t head_bytes = 256ll << args.page_shift;
+  const int64_t page_bytes = head_bytes * args.c.kv_heads;
 
-  if (warp == 4) {
-    // ------------------------------------------------------- producer --
-    if (lane == 0) {
-      prefetch_tmap(&tm_k);
-      prefetch_tmap(&tm_v);
-    }
-    const int boxes = pg::kStage >> args.box_shift;  // per stage: 1, 2 or 4
-    const uint32_t box_bytes = 128u << args.box_shift;
-    int g = 0;
-    bool ok = true;
-    for (int64_t x = x0; x < x1 && ok;) {
-      const Segment s = segment_at(args, x, x1);
-      x += s.n;
-      const int row0 = lane << args.box_shift;  // this lane's box
-      int page = 0;
-      if (lane < boxes)
-        page = page_of(args, s.stream,
-                       static_cast<int64_t>(s.stage0) * pg::kStage + row0);
-      for (int j = 0; j < s.n; ++j, ++g) {
-        const int st = g % kStages, u = g / kStages;
-        if (u > 0) ok = wait_warp(&empty[st], (u - 1) & 1, abort_flag, status);
-        if (!ok) break;
-        if (lane == 0) mbar_expect_tx(&full[st], kStageBytes);
-        __syncwarp();
-        const int64_t pos =
-            static_cast<int64_t>(s.stage0 + j) * pg::kStage + row0;
-        if (lane < boxes) {
-          const int in_page =
-              static_cast<int>(pos) & ((1 << args.page_shift) - 1);
-          uint8_t* dst = smem_raw + (sm - raw) + st * kStageBytes +
-                         lane * box_bytes;
-          tma_load_4d(dst, &tm_k, &full[st], 0, in_page, s.head, page);
-          tma_load_4d(dst + kHalf, &tm_k, &full[st], 64, in_page, s.head,
-                      page);
-          tma_load_4d(dst + 2 * kHalf, &tm_v, &full[st], 0, in_page, s.head,
-                      page);
-          tma_load_4d(dst + 3 * kHalf, &tm_v, &full[st], 64, in_page, s.head,
-                      page);
-          // the next stage's page arrives while this one is loaded
-          if (j + 1 < s.n) page = page_of(args, s.stream, pos + pg::kStage);
-        }
-        __syncwarp();
+  // The loading side: stage lj of segment ls is the next one to fetch.
+  Segment ls = segment_at(args, x0, x1);
+  int lx = x0;
+  int lj = 0, lg = 0;
+  int lpage = page_of(args, ls.stream,
+                      static_cast<int64_t>(ls.stage0) * pg::kStage +
+                          warp * kKeys);
+  const int total_stages = x1 - x0;
+  const uint32_t dst0 = swz(lane >> 4, lane & 15);
+  auto fetch = [&]() {
+    if (lg < total_stages) {
+      const int64_t pos =
+          static_cast<int64_t>(ls.stage0 + lj) * pg::kStage + warp * kKeys;
+      const bool live = lpage < args.c.n_pages;
+      const int64_t off =
+          (live ? lpage * page_bytes + ls.head * head_bytes +
+                      (static_cast<int>(pos) & page_mask) * 256
+                : 0) +
+          lane * 16;
+      const uint32_t st = ring + (lg % kDepth) * (2 * kPart);
+      const char* kg = reinterpret_cast<const char*>(k_pages) + off;
+      const char* vg = reinterpret_cast<const char*>(v_pages) + off;
+      // piece i: rows 2 i and 2 i + 1; their swizzle is (2 i + lane / 16) & 7
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        cp_async16(st + i * 512 + (dst0 ^ ((2 * i & 7) << 4)), kg + i * 512,
+                   live);
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        cp_async16(st + kPart + i * 512 + (dst0 ^ ((2 * i & 7) << 4)),
+                   vg + i * 512, live);
+      ++lg;
+      if (++lj == ls.n) {
+        lx += ls.n;
+        lj = 0;
+        if (lx < x1) ls = segment_at(args, lx, x1);
       }
+      // the next fetch's page arrives while this stage is computed
+      if (lg < total_stages)
+        lpage = page_of(args, ls.stream,
+                        static_cast<int64_t>(ls.stage0 + lj) * pg::kStage +
+                            warp * kKeys);
     }
-    if (*abort_flag) {
-      for (int i = (g > kStages ? g - kStages : 0); i < g; ++i)
-        wait_warp_drain(&full[i % kStages], (i / kStages) & 1, status);
-    }
-    return;
-  }
+    cp_async_commit();  // an empty group keeps the count
+  };
+#pragma unroll
+  for (int i = 0; i < kDepth - 1; ++i) fetch();
 
-  // --------------------------------------------------------- consumers --
   // Fragments of m16n8k16: thread (gr, t4) = (lane / 4, lane % 4) holds rows
   // gr and gr + 8, columns 2 t4, 2 t4 + 1 (+ 8) of A and of the results.
   const int gr = lane >> 2, t4 = lane & 3;
-  const float c2 = args.scale_log2;
-  const int heads = args.c.heads;
   int g = 0;
-  bool ok = true;
-  for (int64_t x = x0; x < x1;) {
+  for (int x = x0; x < x1;) {
     const Segment s = segment_at(args, x, x1);
+    const int4 cfg =
+        __ldg(reinterpret_cast<const int4*>(args.c.streams) + s.stream);
+    const int chunk = cfg.z, window = cfg.w;
     const int rows = min(s.ql * args.group, kRows);
     // rows gr and gr + 8: row r is query head head * group + r % group of
     // new token r / group
@@ -281,8 +335,8 @@ __global__ void __launch_bounds__(kThreads)
       if (!on) orow[e] = -1;
       const int a = s.kv - s.ql + i;
       // a row of padding takes part unmasked and is never written
-      lo[e] = on ? pg::key_lo(max(a, 0), s.chunk, s.window) : 0;
-      hi[e] = on ? pg::key_hi(a, s.chunk, s.kv) : INT32_MAX;
+      lo[e] = on ? pg::key_lo(max(a, 0), chunk, window) : 0;
+      hi[e] = on ? pg::key_hi(a, chunk, s.kv) : INT32_MAX;
       const uint32_t* src = reinterpret_cast<const uint32_t*>(
           args.q + (on ? orow[e] : 0) * HD);
 #pragma unroll
@@ -291,38 +345,42 @@ __global__ void __launch_bounds__(kThreads)
         qf[k][2 + e] = on ? __ldg(src + k * 8 + 4 + t4) : 0u;
       }
     }
-    const int item_lo = pg::key_lo(max(s.kv - s.ql, 0), s.chunk, s.window);
+    const int item_lo = pg::key_lo(max(s.kv - s.ql, 0), chunk, window);
     float o[16][4];
 #pragma unroll
     for (int d = 0; d < 16; ++d)
       o[d][0] = o[d][1] = o[d][2] = o[d][3] = 0.f;
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
     for (int j = 0; j < s.n; ++j, ++g) {
-      const int st = g % kStages;
-      if (ok) ok = wait_warp(&full[st], (g / kStages) & 1, abort_flag, status);
-      if (!ok) continue;
-      const uint32_t ks = sm + st * kStageBytes;
-      const uint32_t vs = ks + 2 * kHalf;
-      const int key0 = (s.stage0 + j) * pg::kStage + warp * 16;
-      // S = Q K^T for this warp's 16 keys: two 8-key tiles
+      __syncwarp();  // the ring slot that is filled next has been read
+      fetch();
+      cp_async_wait<kDepth - 1>();
+      __syncwarp();
+      const uint32_t ks = ring + (g % kDepth) * (2 * kPart);
+      const uint32_t vs = ks + kPart;
+      const int key0 = (s.stage0 + j) * pg::kStage + warp * kKeys;
+      // S = Q K^T: two 8-key tiles, even and odd k-steps in chains of four
       float sc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+      float sd[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
       {
-        const int row = warp * 16 + (lane & 7) + ((lane >> 4) << 3);
+        const int row = (lane & 7) + ((lane >> 4) << 3);
         const int sub = (lane >> 3) & 1;
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-          const int ch = 2 * k + sub;  // 16-byte chunk of the 256-byte row
           uint32_t b[4];
-          ldsm4(ks + (ch >> 3) * kHalf + row * 128 +
-                    (((ch & 7) ^ (row & 7)) << 4),
-                b);
-          mma16816(sc[0], qf[k], b[0], b[1]);
-          mma16816(sc[1], qf[k], b[2], b[3]);
+          ldsm4(ks + swz(row, 2 * k + sub), b);
+          mma16816(k & 1 ? sd[0] : sc[0], qf[k], b[0], b[1]);
+          mma16816(k & 1 ? sd[1] : sc[1], qf[k], b[2], b[3]);
         }
       }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        sc[0][e] += sd[0][e];
+        sc[1][e] += sd[1][e];
+      }
       const bool edge = __any_sync(
-          0xffffffffu, lo[0] > key0 || lo[1] > key0 || hi[0] < key0 + 16 ||
-                           hi[1] < key0 + 16);
+          0xffffffffu, lo[0] > key0 || lo[1] > key0 ||
+                           hi[0] < key0 + kKeys || hi[1] < key0 + kKeys);
       if (edge) {
 #pragma unroll
         for (int n = 0; n < 2; ++n)
@@ -373,7 +431,7 @@ __global__ void __launch_bounds__(kThreads)
       }
       // values outside [item_lo, kv) may be anything: their weight is 0, but
       // 0 * NaN is not.  vm masks this thread's keys 2 t4, + 1 and + 8, + 9.
-      const bool vedge = key0 < item_lo || key0 + 16 > s.kv;
+      const bool vedge = key0 < item_lo || key0 + kKeys > s.kv;
       uint32_t vm[2] = {0xffffffffu, 0xffffffffu};
       if (vedge) {
 #pragma unroll
@@ -384,15 +442,12 @@ __global__ void __launch_bounds__(kThreads)
         }
       }
       {
-        const int row = warp * 16 + (lane & 15);
+        const int row = lane & 15;
         const int sub = lane >> 4;
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-          const int ch = 2 * k + sub;
           uint32_t b[4];
-          ldsm4t(vs + (ch >> 3) * kHalf + row * 128 +
-                     (((ch & 7) ^ (row & 7)) << 4),
-                 b);
+          ldsm4t(vs + swz(row, 2 * k + sub), b);
           if (vedge) {
             b[0] &= vm[0];
             b[1] &= vm[1];
@@ -403,12 +458,9 @@ __global__ void __launch_bounds__(kThreads)
           mma16816(o[2 * k + 1], p, b[2], b[3]);
         }
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&empty[st]);
     }
     // -------------------------------------------- join the four warps --
-    // warps 2, 3 into 0, 1, then 1 into 0; every warp takes every barrier,
-    // also after a wait gave up
+    // warps 2, 3 into 0, 1, then 1 into 0
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
@@ -447,13 +499,13 @@ __global__ void __launch_bounds__(kThreads)
         }
       }
     };
-    named_bar_sync(1, 128);
+    __syncthreads();
     if (warp >= 2) put(join + (warp - 2) * kJoinFloats);
-    named_bar_sync(1, 128);
+    __syncthreads();
     if (warp < 2) take(join + warp * kJoinFloats);
-    named_bar_sync(1, 128);
+    __syncthreads();
     if (warp == 1) put(join);
-    named_bar_sync(1, 128);
+    __syncthreads();
     if (warp == 0) {
       take(join);
       if (s.whole) {
@@ -473,6 +525,7 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const int r = gr + 8 * e;
+          if (orow[e] < 0) continue;
           const int64_t prow = slot * kRows + r;
           if (t4 == 0) args.part_ml[prow] = make_float2(m[e], l[e]);
 #pragma unroll
@@ -491,37 +544,36 @@ __global__ void __launch_bounds__(kThreads)
 __global__ void __launch_bounds__(128)
     paged_few_join(const __grid_constant__ PagedArgs args) {
   const int32_t* work = args.c.work;
-  if (work[pg::H_MODE] != pg::kModeFew) return;
-  const int64_t total = work[pg::H_TOTAL];
-  const int64_t ctas = work[pg::H_CTAS];
+  if (__ldg(work + pg::H_MODE) != pg::kModeFew) return;
   const int kvh = args.c.kv_heads;
+  const int rows = min(args.c.max_new * args.group, kRows);
   const int64_t items =
-      static_cast<int64_t>(work[pg::H_ACTIVE]) * kvh * kRows;
+      static_cast<int64_t>(__ldg(work + pg::H_ACTIVE)) * kvh * rows;
+  if (items == 0) return;
+  const pg::Line line(__ldg(work + pg::H_TOTAL), __ldg(work + pg::H_CTAS));
   const int lane = threadIdx.x & 31;
   const int64_t warps = static_cast<int64_t>(gridDim.x) * 4;
+  grid_dependency_wait();
   for (int64_t it = blockIdx.x * 4ll + (threadIdx.x >> 5); it < items;
        it += warps) {
-    const int r = static_cast<int>(it % kRows);
-    const int64_t ih = it / kRows;
+    const int r = static_cast<int>(it % rows);
+    const int64_t ih = it / rows;
     const int head = static_cast<int>(ih % kvh);
     const int32_t* e = work + pg::kHdr + pg::kEnt * (ih / kvh);
-    const int64_t n = e[pg::E_COUNT];
-    const int64_t xs = e[pg::E_BASE] * static_cast<int64_t>(kvh) + head * n;
-    // CTA c holds [c total / ctas, (c + 1) total / ctas)
-    const int64_t c0 = ((xs + 1) * ctas - 1) / total;
-    const int64_t c1 = ((xs + n) * ctas - 1) / total;
+    const int n = __ldg(e + pg::E_COUNT);
+    const int xs = __ldg(e + pg::E_BASE) * kvh + head * n;
+    const int c0 = line.cta_of(xs), c1 = line.cta_of(xs + n - 1);
     if (c0 == c1) continue;
-    const int stream = e[pg::E_STREAM];
     const int i = r / args.group;
-    const int q0 = args.c.q_start[stream];
-    if (r >= args.c.q_lens[stream] * args.group || q0 + i >= args.c.token_cap)
+    const int q0 = __ldg(e + pg::E_Q0);
+    if (r >= __ldg(e + pg::E_ROWS) * args.group || q0 + i >= args.c.token_cap)
       continue;
     JoinAcc acc;
-    for (int64_t c = c0; c <= c1; ++c) {
-      const int64_t start = c * total / ctas;
-      const int64_t prow = (2 * c + (xs > start ? 1 : 0)) * kRows + r;
-      acc.add(args.part_ml[prow], args.part_o + prow * HD, lane);
-    }
+    // the first CTA's part is its last one unless the item starts it
+    const bool mid = xs > line.first(c0);
+    acc.add_all(c1 - c0 + 1, lane, args, [&](int k) {
+      return (2ll * (c0 + k) + (k == 0 && mid ? 1 : 0)) * kRows + r;
+    });
     acc.write(args.o + ((static_cast<int64_t>(q0) + i) * args.c.heads +
                         head * args.group + (r - i * args.group)) * HD,
               lane);
@@ -1053,6 +1105,7 @@ __global__ void __launch_bounds__(128)
   const int lane = threadIdx.x & 31;
   const int64_t warps = static_cast<int64_t>(gridDim.x) * 4;
   const int heads = args.c.heads;
+  grid_dependency_wait();
   for (int64_t it = blockIdx.x * 4ll + (threadIdx.x >> 5); it < total;
        it += warps) {
     const int32_t* e = find_entry(work, pg::E_ROW, 1, it);
@@ -1064,19 +1117,14 @@ __global__ void __launch_bounds__(128)
     if (row >= args.c.token_cap) continue;
     const int tx = tiles - 1 - i / pg::kTileRows;
     JoinAcc acc;
-    for (int s = 0; s < ns; ++s) {
-      const int64_t slot = e[pg::E_SLOT] + (head * ns + s) * tiles + tx;
-      const int64_t prow = slot * pg::kTileRows + i % pg::kTileRows;
-      acc.add(args.part_ml[prow], args.part_o + prow * HD, lane);
-    }
+    const int64_t slot0 = e[pg::E_SLOT] + head * ns * tiles + tx;
+    acc.add_all(ns, lane, args, [&](int k) {
+      return (slot0 + k * tiles) * pg::kTileRows + i % pg::kTileRows;
+    });
     acc.write(args.o + (row * heads + head) * HD, lane);
   }
 }
 }  // namespace tile
-
-int paged_box_rows(const wan_paged_t* c) {
-  return c->page_size < 64 ? c->page_size : 64;
-}
 
 int paged_log2(int v) {
   int s = 0;
@@ -1102,8 +1150,26 @@ int paged_slot_rows(const wan_paged_t* c) {
   return pg::few_mode(c) ? pg::kFewRows : pg::kTileRows;
 }
 
-int launch_few(const CUtensorMap& mk, const CUtensorMap& mv,
-               const PagedArgs& a, int sms, cudaStream_t s) {
+// Launches a joining kernel behind the kernel just launched on s: its CTAs
+// may start while that one still runs and wait for its end in
+// grid_dependency_wait.
+int launch_join(void (*kern)(PagedArgs), int64_t blocks, const PagedArgs& a,
+                cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks));
+  cfg.blockDim = dim3(128);
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, a) == cudaSuccess ? WAN_OK
+                                                          : WAN_ECUDA;
+}
+
+int launch_few(const void* k_pages, const void* v_pages, const PagedArgs& a,
+               int sms, cudaStream_t s) {
   static std::mutex mu;
   static bool ready[64];
   int dev = 0;
@@ -1120,17 +1186,17 @@ int launch_few(const CUtensorMap& mk, const CUtensorMap& mv,
     }
   }
   few::paged_few_kernel<<<pg::kFewCtasPerSm * sms, few::kThreads, few::kSmem,
-                          s>>>(mk, mv, a);
+                          s>>>(static_cast<const __nv_bfloat16*>(k_pages),
+                               static_cast<const __nv_bfloat16*>(v_pages), a);
   if (cudaGetLastError() != cudaSuccess) return WAN_ECUDA;
-  const int64_t rows =
-      static_cast<int64_t>(a.c.n_streams) * a.c.kv_heads * pg::kFewRows;
+  const int64_t rows = static_cast<int64_t>(a.c.n_streams) * a.c.kv_heads *
+                       a.c.max_new * a.group;
   int64_t blocks = (rows + 3) / 4;
   if (blocks > 8ll * sms) blocks = 8ll * sms;
-  few::paged_few_join<<<static_cast<unsigned>(blocks), 128, 0, s>>>(a);
-  return cudaGetLastError() == cudaSuccess ? WAN_OK : WAN_ECUDA;
+  return launch_join(few::paged_few_join, blocks, a, s);
 }
 
-int launch_tile(const CUtensorMap& mk, const CUtensorMap& mv,
+int launch_tile(const void* k_pages, const void* v_pages,
                 const PagedArgs& a, int sms, cudaStream_t s) {
   static std::mutex mu;
   static int state[64];  // 0 unknown, 1 ready, 2 unusable
@@ -1158,13 +1224,18 @@ int launch_tile(const CUtensorMap& mk, const CUtensorMap& mv,
     }
     if (state[dev] != 1) return WAN_EUNSUPPORTED;
   }
-  CUtensorMap mq;
-  const int st = make_map_bf16(&mq, a.q, 1, a.c.token_cap, a.c.heads, BM);
+  CUtensorMap mq, mk, mv;
+  int st = make_map_bf16(&mq, a.q, 1, a.c.token_cap, a.c.heads, BM);
   if (st != WAN_OK) return st;
+  const int box = 1 << a.box_shift;
+  if ((st = make_map_pages(&mk, k_pages, a.c.n_pages, a.c.kv_heads,
+                           a.c.page_size, box)) != WAN_OK ||
+      (st = make_map_pages(&mv, v_pages, a.c.n_pages, a.c.kv_heads,
+                           a.c.page_size, box)) != WAN_OK)
+    return st;
   tile::paged_tile_kernel<<<sms, kThreads, SMEM_DYN, s>>>(mq, mk, mv, a);
   if (cudaGetLastError() != cudaSuccess) return WAN_ECUDA;
-  tile::paged_tile_join<<<8 * sms, 128, 0, s>>>(a);
-  return cudaGetLastError() == cudaSuccess ? WAN_OK : WAN_ECUDA;
+  return launch_join(tile::paged_tile_join, 8ll * sms, a, s);
 }
 
 }  // namespace
@@ -1196,14 +1267,6 @@ int wan_paged_attn(const wan_paged_t* c, const void* q, const void* k_pages,
   const int sms = paged_sms();
   if (sms < 1) return WAN_ECUDA;
   if (workspace_bytes < wan_paged_workspace_bytes(c)) return WAN_ENOSPACE;
-  const int box = paged_box_rows(c);
-  CUtensorMap mk, mv;
-  if ((st = make_map_pages(&mk, k_pages, c->n_pages, c->kv_heads,
-                           c->page_size, box)) != WAN_OK)
-    return st;
-  if ((st = make_map_pages(&mv, v_pages, c->n_pages, c->kv_heads,
-                           c->page_size, box)) != WAN_OK)
-    return st;
   PagedArgs a;
   a.c = *c;
   a.q = static_cast<const __nv_bfloat16*>(q);
@@ -1214,9 +1277,10 @@ int wan_paged_attn(const wan_paged_t* c, const void* q, const void* k_pages,
   a.scale_log2 = softmax_scale * 1.4426950408889634f;
   a.group = c->heads / c->kv_heads;
   a.page_shift = paged_log2(c->page_size);
-  a.box_shift = paged_log2(box);
-  return paged::few_mode(c) ? launch_few(mk, mv, a, sms, as_stream(s))
-                            : launch_tile(mk, mv, a, sms, as_stream(s));
+  a.box_shift = paged_log2(c->page_size < 64 ? c->page_size : 64);
+  return paged::few_mode(c)
+             ? launch_few(k_pages, v_pages, a, sms, as_stream(s))
+             : launch_tile(k_pages, v_pages, a, sms, as_stream(s));
 }
 
 }  // extern "C"
