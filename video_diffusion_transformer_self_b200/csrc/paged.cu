@@ -57,6 +57,21 @@ namespace {
 // another kernel.
 constexpr int kPlanThreads = 1024;
 
+// Division of 0 <= n < 2^31 by 1 <= d < 2^31 as (n * m) >> (31 + s) with
+// s = ceil(log2 d), m = floor(2^(31 + s) / d) + 1: m exceeds 2^(31 + s) / d
+// by at most 1, which adds less than n 2^-(31 + s) < 2^-s <= 1 / d to the
+// quotient, too little to reach the next whole number.
+__device__ __forceinline__ uint32_t div_magic(int d) {
+  const int s = d > 1 ? 32 - __clz(d - 1) : 0;
+  return static_cast<uint32_t>((1ull << (31 + s)) / static_cast<uint32_t>(d)) +
+         1u;
+}
+__device__ __forceinline__ int div_by(int n, int d, uint32_t m) {
+  const int s = d > 1 ? 32 - __clz(d - 1) : 0;
+  return static_cast<int>(
+      (static_cast<uint64_t>(static_cast<uint32_t>(n)) * m) >> (31 + s));
+}
+
 struct PlanArgs {
   wan_paged_t c;
   const int32_t* new_lens;
@@ -64,6 +79,14 @@ struct PlanArgs {
   int sms;
   int few;
 };
+
+// Cluster barrier in two halves.
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
 
 __device__ __forceinline__ uint64_t block_scan(uint64_t v, uint64_t* red) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -109,6 +132,7 @@ __device__ __forceinline__ int find_stream(const int* incl, int n, int x) {
 constexpr int kUnitCost = 3;
 constexpr int kJoinCost = 2;
 constexpr int kSlotsPerBlock = 50;
+constexpr int kManyWaves = 16;
 constexpr int kMinStages = 1;  // stages of a CTA on the few-row kernel
 constexpr int kMinRange = 8;  // key blocks of a range
 
@@ -161,31 +185,61 @@ __device__ void build_work(const PlanArgs& a, int ql, int kv, int q0,
     if (nb < 1) nb = 1;
   }
   // streams by falling length: CTA i takes units i, i + G, ... so its share
-  // is heaviest for i = 0 and within one unit of the lightest
-  s_a[r] = nb;
-  __syncthreads();
-  int rank = 0;
-  for (int i = 0; i < c.n_streams; ++i) {
-    const int o = s_a[i];
-    rank += (o > nb || (o == nb && i < r)) ? 1 : 0;
-  }
+  // is heaviest for i = 0 and within one unit of the lightest.  Keys hold
+  // the length (capped, which only changes the order) over the place; a
+  // bitonic network of shuffles and, across warps, shared memory sorts them.
   const int n_act = __syncthreads_count(on);
   const int tiles = (ql + kTileRows - 1) / kTileRows;
-  __syncthreads();
-  if (on) {
-    s_a[rank] = nb;
-    s_b[rank] = tiles;
-    s_c[rank] = r;
+  uint32_t key = on ? (static_cast<uint32_t>(min(nb, (1 << 22) - 1)) << 10) |
+                          static_cast<uint32_t>(kMaxStreams - 1 - r)
+                    : 0u;
+  uint32_t* s_key = reinterpret_cast<uint32_t*>(s_a);
+  if (c.n_streams > 1) {
+    for (int k = 2; k <= kMaxStreams; k <<= 1) {
+      for (int j = k >> 1; j > 0; j >>= 1) {
+        uint32_t other;
+        if (j >= 32) {
+          __syncthreads();
+          s_key[r] = key;
+          __syncthreads();
+          other = s_key[r ^ j];
+        } else {
+          other = __shfl_xor_sync(0xffffffffu, key, j);
+        }
+        // falling order where bit k of r is clear
+        const bool keep_max = ((r & k) == 0) == ((r & j) == 0);
+        key = keep_max ? max(key, other) : min(key, other);
+      }
+    }
   }
+  const int src = kMaxStreams - 1 - static_cast<int>(key & (kMaxStreams - 1));
+  // stream src is the r-th longest
   __syncthreads();
-  // warp w tries ranges of at most 1 / (w + 1) of the longest stream
+  s_a[r] = nb;
+  s_b[r] = tiles;
+  s_c[r] = ql;
+  __syncthreads();
+  const bool mine = r < n_act;
+  const int m_nb = mine ? s_a[src] : 0;
+  const int m_tiles = mine ? s_b[src] : 0;
+  const int m_ql = mine ? s_c[src] : 0;
+  __syncthreads();
+  s_a[r] = m_nb;
+  s_b[r] = m_tiles;
+  const int64_t whole = static_cast<int64_t>(block_scan(
+      static_cast<uint64_t>(m_tiles) * c.heads, red));
+  __shared__ int s_many;
+  if (r == blockDim.x - 1) s_many = whole >= kManyWaves * a.sms;
+  __syncthreads();
+  // warp w tries ranges of at most 1 / (w + 1) of the longest stream; with
+  // many waves of units there is nothing to gain
   const int lane = r & 31, w = r >> 5;
   const int longest = n_act ? s_a[0] : 0;
   const int range = (longest + w) / (w + 1);
   int64_t cost = INT64_MAX;
-  if (n_act && (w == 0 || range >= kMinRange)) {
+  if (n_act && (w == 0 || (range >= kMinRange && !s_many))) {
     int64_t t = 0, base = 0, slots = 0;
-    for (int i0 = 0; i0 < n_act; i0 += 32) {
+    for (int i0 = 0; i0 < n_act && !(s_many && w == 0); i0 += 32) {
       const int i = i0 + lane;
       int64_t units = 0;
       int len = 0, ns = 1;
@@ -200,9 +254,14 @@ __device__ void build_work(const PlanArgs& a, int ql, int kv, int q0,
         const int64_t u = __shfl_up_sync(0xffffffffu, incl, o);
         if (lane >= o) incl += u;
       }
-      const int64_t p0 = base + incl - units, p1 = base + incl;
-      const int64_t cnt = (p1 + a.sms - 1) / a.sms - (p0 + a.sms - 1) / a.sms;
-      t += cnt * (len + kUnitCost);
+      // units of CTA 0 among p0 .. p1 - 1 (capped: a list that long is one
+      // of whole units, whose cost is not compared)
+      const uint32_t p1 =
+          static_cast<uint32_t>(min(base + incl, static_cast<int64_t>(1) << 30));
+      const uint32_t p0 = static_cast<uint32_t>(
+          min(base + incl - units, static_cast<int64_t>(1) << 30));
+      const uint32_t cnt = (p1 + a.sms - 1) / a.sms - (p0 + a.sms - 1) / a.sms;
+      t += static_cast<int64_t>(cnt) * (len + kUnitCost);
       if (ns > 1) slots += units;
       base += __shfl_sync(0xffffffffu, incl, 31);
     }
@@ -217,32 +276,30 @@ __device__ void build_work(const PlanArgs& a, int ql, int kv, int q0,
   }
   if (lane == 0) s_cost[w] = cost;
   __syncthreads();
-  int best = 0;
-  for (int i = 1; i < 32; ++i)
-    if (s_cost[i] < s_cost[best]) best = i;
-  const int rng = (longest + best) / (best + 1);
-  // entry r of the list
-  int ns = 1;
-  uint64_t units = 0, slots = 0, rows = 0;
-  int src = 0;
-  if (r < n_act) {
-    ns = (s_a[r] + rng - 1) / rng;
-    src = s_c[r];
-    units = static_cast<uint64_t>(s_b[r]) * c.heads * ns;
-    if (ns > 1) slots = units;
+  int64_t low = s_cost[lane];
+  int best = lane;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const int64_t lo2 = __shfl_xor_sync(0xffffffffu, low, o);
+    const int b2 = __shfl_xor_sync(0xffffffffu, best, o);
+    if (lo2 < low || (lo2 == low && b2 < best)) {
+      low = lo2;
+      best = b2;
+    }
   }
-  __syncthreads();
-  s_a[r] = ql;
-  __syncthreads();
-  if (r < n_act && ns > 1)
-    rows = static_cast<uint64_t>(s_a[src]) * c.heads;
+  const int rng = max((longest + best) / (best + 1), 1);
+  // entry r of the list
+  const int ns = mine ? (m_nb + rng - 1) / rng : 1;
+  const uint64_t units = static_cast<uint64_t>(m_tiles) * c.heads * ns;
+  const uint64_t slots = ns > 1 ? units : 0;
+  const uint64_t rows = ns > 1 ? static_cast<uint64_t>(m_ql) * c.heads : 0;
   const uint64_t su = block_scan((units << 32) | slots, red);
   const uint64_t sr = block_scan(rows, red);
-  if (r < n_act) {
+  if (mine) {
     int32_t* e = work + kHdr + kEnt * r;
     e[E_STREAM] = src;
     e[E_BASE] = static_cast<int>((su >> 32) - units);
-    e[E_COUNT] = s_b[r];
+    e[E_COUNT] = m_tiles;
     e[E_SPLIT] = ns;
     e[E_SLOT] = static_cast<int>((su & 0xFFFFFFFFull) - slots);
     e[E_ROW] = static_cast<int>(sr - rows);
@@ -266,6 +323,10 @@ __global__ void __launch_bounds__(kPlanThreads)
   __shared__ int s_need[kMaxStreams];   // pages going out, inclusive
   __shared__ int s_old[kMaxStreams];    // tokens before the step
   __shared__ int s_from[kMaxStreams];   // first page coming back
+  __shared__ int s_hw[kMaxStreams];     // tokens of a frame and of a row,
+  __shared__ int s_w[kMaxStreams];      //   with their div_magic
+  __shared__ uint32_t s_mhw[kMaxStreams];
+  __shared__ uint32_t s_mw[kMaxStreams];
   const wan_paged_t& c = a.c;
   const int R = c.n_streams;
   const int r = threadIdx.x;
@@ -322,29 +383,47 @@ __global__ void __launch_bounds__(kPlanThreads)
   const bool admit = valid && need_incl <= free_now;
   s_need[r] = need_incl;
   s_rows[r] = admit ? rows : 0;
+  if (admit) {  // H and W lie in the grid, so H W <= 2^20
+    s_hw[r] = cfg.x * cfg.y;
+    s_w[r] = cfg.y;
+    s_mhw[r] = div_magic(cfg.x * cfg.y);
+    s_mw[r] = div_magic(cfg.y);
+  }
   // admission stops for good at the first stream that does not fit, so the
   // admitted needs are a prefix of the line of needs
   const int n_out = static_cast<int>(
       block_scan(admit ? static_cast<uint64_t>(need) : 0ull, red));
   __shared__ int s_out;
   if (r == kPlanThreads - 1) s_out = n_out;
+  const int kv = ended ? 0 : old + (admit ? rows : 0);
   const int ctas = gridDim.x;
   const int rank = blockIdx.x;
-  const int step = ctas * kPlanThreads;
+  // with a cluster its last CTA divides the attention's work (no global
+  // state but its own output) and the others do the moves
+  const int movers = ctas > 1 ? ctas - 1 : 1;
+  const int step = movers * kPlanThreads;
   const int me = rank * kPlanThreads + r;
-  for (int i = me; i < n_back; i += step) {
-    const int q = find_stream(s_back, R, i);
-    const int at = i - (q ? s_back[q - 1] : 0);
-    int32_t* ent = c.block_table +
-                   static_cast<int64_t>(q) * c.max_pages + s_from[q] + at;
-    c.free_ring[(head + static_cast<uint32_t>(count) + i) % np] = *ent;
-    *ent = -1;
+  if (rank < movers) {
+    for (int i = me; i < n_back; i += step) {
+      const int q = find_stream(s_back, R, i);
+      const int at = i - (q ? s_back[q - 1] : 0);
+      int32_t* ent = c.block_table +
+                     static_cast<int64_t>(q) * c.max_pages + s_from[q] + at;
+      c.free_ring[(head + static_cast<uint32_t>(count) + i) % np] = *ent;
+      *ent = -1;
+    }
   }
-  __syncwarp();
-  if (ctas > 1)
-    cluster_sync_all();
-  else
+  __syncthreads();
+  if (ctas > 1) cluster_arrive();
+  if (rank == movers) {
+    build_work(a, admit ? rows : 0, kv, r ? s_end[r - 1] : 0, cfg.z, cfg.w,
+               red, s_back, s_need, s_from, s_cost);
     __syncthreads();
+    cluster_wait();
+    return;
+  }
+  // once all pages are back and all CTAs have read the old state
+  if (ctas > 1) cluster_wait();
   const int out = s_out;
   for (int i = me; i < out; i += step) {
     const int q = find_stream(s_need, R, i);
@@ -353,37 +432,6 @@ __global__ void __launch_bounds__(kPlanThreads)
     c.block_table[static_cast<int64_t>(q) * c.max_pages + p] =
         c.free_ring[(head + i) % np];
   }
-  // the tokens' records: the page of a new position is either one the stream
-  // held (its table entry does not change) or comes from the ring
-  int4* tok = reinterpret_cast<int4*>(c.tokens);
-  const int n_rows = s_end[R - 1];
-  for (int i = me; i < c.token_cap; i += step) {
-    int4 rec = make_int4(0, 0, 0, -1);
-    if (i < n_rows) {
-      const int q = find_stream(s_end, R, i);
-      // rows of the stream start where those of the one before end
-      const int off = i - (q ? s_end[q - 1] : 0);
-      if (off < s_rows[q]) {
-        const int pos = s_old[q] + off;
-        const int4 f = __ldg(reinterpret_cast<const int4*>(c.streams) + q);
-        const int hw = f.x * f.y;
-        rec.x = pos / hw;
-        const int rest = pos - rec.x * hw;
-        rec.y = rest / f.y;
-        rec.z = rest - rec.y * f.y;
-        const int p = pos >> a.page_shift;
-        const int h0 = (s_old[q] + ps - 1) >> a.page_shift;
-        int page;
-        if (p < h0)
-          page = c.block_table[static_cast<int64_t>(q) * c.max_pages + p];
-        else
-          page = c.free_ring[(head + (q ? s_need[q - 1] : 0) + (p - h0)) % np];
-        rec.w = (page << a.page_shift) + (pos & (ps - 1));
-      }
-    }
-    tok[i] = rec;
-  }
-  const int kv = ended ? 0 : old + (admit ? rows : 0);
   if (rank == 0) {
     if (r < R) {
       c.kv_lens[r] = kv;
@@ -401,11 +449,46 @@ __global__ void __launch_bounds__(kPlanThreads)
       c.ring_state[1] = free_now - out;
     }
   }
-  // the last CTA has no state to write
-  if (rank == ctas - 1) {
+  // The tokens' records: the page of a new position is either one the stream
+  // held (its table entry does not change) or comes from the ring.  A warp
+  // takes consecutive records, so that its stream moves on by a step or two
+  // between them; divisions by a stream's frame and row are multiplications.
+  int4* tok = reinterpret_cast<int4*>(c.tokens);
+  const int n_rows = s_end[R - 1];
+  const int warps = movers * (kPlanThreads / 32);
+  const int share = ((c.token_cap + warps - 1) / warps + 31) & ~31;
+  const int i0 = (me >> 5) * share;
+  const int i1 = min(i0 + share, c.token_cap);
+  int q = i0 < n_rows ? find_stream(s_end, R, min(i0 + (r & 31), n_rows - 1))
+                      : 0;
+  for (int i = i0 + (r & 31); i < i1; i += 32) {
+    int4 rec = make_int4(0, 0, 0, -1);
+    if (i < n_rows) {
+      while (s_end[q] <= i) ++q;
+      // rows of the stream start where those of the one before end
+      const int off = i - (q ? s_end[q - 1] : 0);
+      if (off < s_rows[q]) {
+        const int pos = s_old[q] + off;
+        rec.x = div_by(pos, s_hw[q], s_mhw[q]);
+        const int rest = pos - rec.x * s_hw[q];
+        rec.y = div_by(rest, s_w[q], s_mw[q]);
+        rec.z = rest - rec.y * s_w[q];
+        const int p = pos >> a.page_shift;
+        const int h0 = (s_old[q] + ps - 1) >> a.page_shift;
+        int page;
+        if (p < h0)
+          page = c.block_table[static_cast<int64_t>(q) * c.max_pages + p];
+        else
+          page = c.free_ring[(head + (q ? s_need[q - 1] : 0) + (p - h0)) % np];
+        rec.w = (page << a.page_shift) + (pos & (ps - 1));
+      }
+    }
+    tok[i] = rec;
+  }
+  if (ctas == 1) {
     __syncthreads();
-    build_work(a, admit ? rows : 0, kv, r ? s_end[r - 1] : 0, cfg.z, cfg.w, red, s_back, s_need,
-               s_from, s_cost);
+    build_work(a, admit ? rows : 0, kv, r ? s_end[r - 1] : 0, cfg.z, cfg.w,
+               red, s_back, s_need, s_from, s_cost);
   }
 }
 
@@ -416,7 +499,10 @@ __global__ void __launch_bounds__(kPlanThreads)
 // l >> 4 + 2, ... in registers (kRows of them), so a row is one batch of
 // independent loads, one reduction and one batch of stores; a head's 256
 // bytes land contiguously in its page.  For more than 2 * 20 heads the row
-// is read twice (the second time from L2).
+// is read twice (the second time from L2).  One item a warp and as many CTAs
+// as that takes: new CTAs load while others store, where a warp that walked
+// several items alternated between the two (43,200 rows x 40 heads, 2.65 GB:
+// 446 us walking, 414 us so, 6.4 TB/s; 3 CTAs an SM instead of 4: 499 us).
 constexpr int kWrThreads = 128;
 constexpr int kWrWarps = kWrThreads / 32;
 constexpr int kWrMaxRows = 20;
@@ -437,7 +523,7 @@ struct WriteArgs {
 
 template <int kRows>
 constexpr int wr_min_blocks() {
-  return kRows <= 4 ? 8 : kRows <= 8 ? 6 : kRows <= 12 ? 5 : 3;
+  return kRows <= 4 ? 8 : kRows <= 8 ? 6 : kRows <= 12 ? 5 : 4;
 }
 
 // kRows 0: any head count, two passes over the row.
@@ -448,19 +534,16 @@ __launch_bounds__(kWrThreads, kRows ? wr_min_blocks<kRows>() : 8)
   const int lane = threadIdx.x & 31;
   const int c = lane & 15;
   const int hsub = lane >> 4;
-  const int64_t stride = static_cast<int64_t>(gridDim.x) * kWrWarps;
-  const int64_t items = 3ll * a.rows;
-  for (int64_t it = static_cast<int64_t>(blockIdx.x) * kWrWarps +
-                    (threadIdx.x >> 5);
-       it < items; it += stride) {
-    const int row = static_cast<int>(it / 3);
-    const int which = static_cast<int>(it - 3ll * row);
+  const unsigned it = blockIdx.x * kWrWarps + (threadIdx.x >> 5);
+  const int row = static_cast<int>(it / 3);
+  const int which = static_cast<int>(it - 3u * row);
+  if (row < a.rows) {
     const int4 tk = __ldg(a.tokens + row);
     // rows of no stream, and records that no plan writes
     if (tk.w < 0 || tk.w >= a.slots || static_cast<unsigned>(tk.x) >= a.F ||
         static_cast<unsigned>(tk.y) >= a.H ||
         static_cast<unsigned>(tk.z) >= a.W)
-      continue;
+      return;
     const int nh = which == 0 ? a.heads : a.kv_heads;
     // selects, not indexes: a runtime index into the parameters would copy
     // them to the stack
@@ -499,7 +582,7 @@ __launch_bounds__(kWrThreads, kRows ? wr_min_blocks<kRows>() : 8)
       } else {
         for (int h = hsub; h < nh; h += 2) out[h * hstep] = in[h * 16];
       }
-      continue;
+      return;
     }
     const float4* tt = a.table + static_cast<int64_t>(tk.x) * 11;
     const float4* th = a.table + static_cast<int64_t>(a.F + tk.y) * 11;
@@ -645,11 +728,7 @@ int wan_paged_write(const wan_paged_t* c, const void* q, void* q_out,
       : c->heads <= 2 * kWrMaxRows
           ? paged_write_kernel<kWrMaxRows>
           : paged_write_kernel<0>;
-  const int cap =
-      resident_grid(reinterpret_cast<const void*>(kern), kWrThreads, dev);
-  if (cap < 1) return WAN_ECUDA;
-  int64_t blocks = (3ll * a.rows + kWrWarps - 1) / kWrWarps;
-  if (blocks > cap) blocks = cap;
+  const int64_t blocks = (3ll * a.rows + kWrWarps - 1) / kWrWarps;
   kern<<<static_cast<unsigned>(blocks), kWrThreads, 0, as_stream(s)>>>(a);
   return cudaGetLastError() == cudaSuccess ? WAN_OK : WAN_ECUDA;
 }
