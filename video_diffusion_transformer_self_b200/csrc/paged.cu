@@ -6,6 +6,8 @@
 // source reading, ch. 4, section "3D RoPE": q and k pass an RMSNorm, then
 // turn by the token's frame, row and column.  The calls and their layouts
 // are described in wan.h.
+#include <mutex>
+
 #include "paged.cuh"
 #include "rope_common.cuh"
 
@@ -124,207 +126,250 @@ __device__ __forceinline__ int find_stream(const int* incl, int n, int x) {
   return lo;
 }
 
-// Makespan of a division of the tile kernel's work, in 128-key blocks, and
-// the constants it is estimated with: a unit costs its blocks and about 3
-// more (Q load, first scores, output), a split call 2 more for the combining
-// pass and 1/50 for each partial result (133 KB written and read at memory
-// speed).
-constexpr int kUnitCost = 3;
-constexpr int kJoinCost = 2;
-constexpr int kSlotsPerBlock = 50;
-constexpr int kManyWaves = 16;
-constexpr int kMinStages = 1;  // stages of a CTA on the few-row kernel
-constexpr int kMinRange = 8;  // key blocks of a range
+// Scratch of build_work, one entry a stream or CTA.
+struct WorkMem {
+  int *a, *b, *c, *d;
+  unsigned long long* load;
+};
+
+// The few-row kernel's line: 64-key stages from the first row's first key to
+// the end of the stream; at least one, so that rows that see nothing are
+// written too.
+__device__ void build_few(const PlanArgs& a, int ql, int kv, int q0, int lo,
+                          uint64_t* red) {
+  const int r = threadIdx.x;
+  int32_t* work = a.c.work;
+  const bool on = ql > 0;
+  const int stage0 = on ? min(lo, kv - 1) / kStage : 0;
+  const int n = on ? (kv + kStage - 1) / kStage - stage0 : 0;
+  const uint64_t sc = block_scan(
+      (static_cast<uint64_t>(on) << 40) | static_cast<uint64_t>(n), red);
+  const int idx = static_cast<int>(sc >> 40) - on;
+  const int base = static_cast<int>(sc & 0xFFFFFFFFFFull) - n;
+  if (on) {
+    int32_t* e = work + kHdr + kEnt * idx;
+    e[E_STREAM] = r;
+    e[E_BASE] = base;
+    e[E_COUNT] = n;
+    e[E_STAGE0] = stage0;
+    e[E_KV] = kv;
+    e[E_ROWS] = ql;
+    e[E_Q0] = q0;
+  }
+  if (r == blockDim.x - 1) {
+    const int64_t total = static_cast<int64_t>(base + n) * a.c.kv_heads;
+    const int64_t most = static_cast<int64_t>(a.sms) * kFewCtasPerSm;
+    work[H_MODE] = kModeFew;
+    work[H_ACTIVE] = idx + on;
+    work[H_TOTAL] = static_cast<int>(total);
+    work[H_CTAS] = static_cast<int>(total < 1 ? 1 : total > most ? most : total);
+    work[H_WAVES] = 0;
+  }
+}
+
+// Orders the streams with rows by falling length: thread i gets the i-th's
+// number (of n_act; any number past them).
+__device__ __forceinline__ int sorted_stream(int n_streams, bool on, int nb,
+                                             int* mem) {
+  const int r = threadIdx.x;
+  // Keys hold the length (capped, which only changes the order) over the
+  // place; a bitonic network of shuffles and, across warps, shared memory.
+  uint32_t key = on ? (static_cast<uint32_t>(min(nb, (1 << 22) - 1)) << 10) |
+                          static_cast<uint32_t>(kMaxStreams - 1 - r)
+                    : 0u;
+  uint32_t* s_key = reinterpret_cast<uint32_t*>(mem);
+  const int top = n_streams <= 32 ? 32 : kMaxStreams;
+  for (int k = 2; k <= top; k <<= 1) {
+    for (int j = k >> 1; j > 0; j >>= 1) {
+      uint32_t other;
+      if (j >= 32) {
+        __syncthreads();
+        s_key[r] = key;
+        __syncthreads();
+        other = s_key[r ^ j];
+      } else {
+        other = __shfl_xor_sync(0xffffffffu, key, j);
+      }
+      // falling order where bit k of r is clear (up to 32 streams: in the
+      // first warp, whose bit 5 is)
+      const bool keep_max = ((r & k) == 0) == ((r & j) == 0);
+      key = keep_max ? max(key, other) : min(key, other);
+    }
+  }
+  return kMaxStreams - 1 - static_cast<int>(key & (kMaxStreams - 1));
+}
+
+// Weights of a stream's units: nb key blocks, ql rows.
+__device__ __forceinline__ int full_weight(int nb) {
+  return kPairWeight * nb + kUnitWeight;
+}
+__device__ __forceinline__ int last_weight(int nb, int ql) {
+  const int rest = ql & (kTileRows - 1);
+  return (rest >= 1 && rest <= kBlock ? kOneWeight : kPairWeight) * nb +
+         kUnitWeight;
+}
+
+// The tile kernel's division of the work.  Whole units in rounds over the
+// CTAs keep neighbours on the same head and keys in step (their K and V
+// blocks are read once into L2); a last round that is not full would leave
+// SMs idle (760 units on 148 SMs are 5.14 rounds: 14 % of the time), so the
+// last one to two rounds' units are cut by weight instead.
+__device__ void build_tiles(const PlanArgs& a, int ql, int nb, uint64_t* red,
+                            const WorkMem& mem) {
+  const int r = threadIdx.x;
+  const bool on = ql > 0;
+  const int heads = a.c.heads;
+  __shared__ int s_units, s_act;
+  __shared__ unsigned long long s_top, s_sum;
+  unsigned long long* s_load = mem.load;
+  const int src = sorted_stream(a.c.n_streams, on, nb, mem.a);
+  const int n_act = __syncthreads_count(on);
+  mem.a[r] = nb;
+  mem.b[r] = ql;
+  if (r == 0) mem.c[0] = 0;
+  __syncthreads();
+  if (on) atomicMax(&mem.c[0], nb);
+  __syncthreads();
+  const bool mine = r < n_act;
+  const int m_nb = mine ? mem.a[src] : 0;
+  const int m_ql = mine ? mem.b[src] : 0;
+  const int m_tiles = (m_ql + kTileRows - 1) / kTileRows;
+  // (lengths past 65,535 blocks are scaled so that the line fits 32 bits)
+  const int down = max(0, 16 - __clz(mem.c[0]));
+  const int w_nb = m_nb >> down;
+  const int m_full = full_weight(w_nb), m_last = last_weight(w_nb, m_ql);
+  const int units = m_tiles * heads;
+  const int upto =
+      static_cast<int>(block_scan(static_cast<uint64_t>(units), red));
+  const uint64_t weight =
+      mine ? static_cast<uint64_t>(heads) *
+                 (static_cast<uint64_t>(m_tiles - 1) * m_full + m_last)
+           : 0;
+  const uint64_t all = block_scan(weight, red);
+  __syncthreads();
+  mem.a[r] = upto;           // units up to and with the r-th stream
+  mem.b[r] = m_tiles;
+  mem.c[r] = m_full;
+  mem.d[r] = m_last;
+  if (r == kPlanThreads - 1) {
+    s_units = upto;
+    s_act = n_act;
+    s_sum = all;
+  }
+  __syncthreads();
+  const int U = s_units;
+  // fewer CTAs where there is not enough for all: 4 blocks each
+  const int64_t parts = static_cast<int64_t>(s_sum) / (kPairWeight * 4);
+  int G = a.sms;
+  if (U < G) G = static_cast<int>(min(static_cast<int64_t>(G),
+                                      max(static_cast<int64_t>(U), parts)));
+  if (G < 1) G = 1;
+  // Loads of the CTAs after K rounds; the most rounds whose heaviest CTA
+  // stays within the mean (at most two fewer than there are: the rounds go
+  // up and down, which leaves little beyond the last unit's length).
+  const int share = kPlanThreads / G;  // threads of one CTA's sum
+  const int c = r % G, part = r / G;
+  int K = U / G;
+  for (int tries = 0;; ++tries) {
+    if (r < G) s_load[r] = 0;
+    if (r == 0) s_top = 0;
+    __syncthreads();
+    if (part < share) {
+      unsigned long long sum = 0;
+      for (int k = part; k < K; k += share) {
+        const int u = k * G + (k & 1 ? G - 1 - c : c);
+        const int i = find_stream(mem.a, n_act, u);
+        const int at = u - (i ? mem.a[i - 1] : 0);
+        sum += at % mem.b[i] == 0 ? mem.d[i] : mem.c[i];
+      }
+      atomicAdd(&s_load[c], sum);
+    }
+    __syncthreads();
+    if (r < G) atomicMax(&s_top, s_load[r]);
+    __syncthreads();
+    if (K == 0 || tries == 2 || s_top * G <= s_sum) break;
+    --K;
+    __syncthreads();
+  }
+  // the line: places in proportion to what each CTA lacks
+  const uint64_t mean = (s_sum + G - 1) / G;
+  const uint64_t lack =
+      r < G && s_load[r] < mean ? mean - s_load[r] : 0;
+  const uint64_t lack_upto = block_scan(lack, red);
+  const int first = K * G;  // units before the line
+  const int base = upto - units;
+  // ragged pairs (every m_tiles-th unit, the first of a head) among the
+  // stream's units before the line
+  const int before = min(max(first - base, 0), units);
+  const int rag = mine ? (before + m_tiles - 1) / m_tiles : 0;
+  const uint64_t skipped = static_cast<uint64_t>(before - rag) * m_full +
+                           static_cast<uint64_t>(rag) * m_last;
+  const uint64_t on_line = weight - (mine ? skipped : 0);
+  const uint64_t line_upto = block_scan(on_line, red);
+  __shared__ unsigned long long s_lack, s_line;
+  if (r == kPlanThreads - 1) {
+    s_lack = lack_upto;
+    s_line = line_upto;
+  }
+  __syncthreads();
+  int32_t* work = a.c.work;
+  if (r < G) {
+    // (the line and the lacks are below 2^30: three rounds of weights)
+    work[kLine + r + 1] =
+        r == G - 1 ? static_cast<int>(s_line)
+                   : static_cast<int>(s_lack ? s_line * lack_upto / s_lack : 0);
+    if (r == 0) work[kLine] = 0;
+  }
+  if (mine) {
+    int32_t* e = work + kHdr + kEnt * r;
+    e[E_STREAM] = src;
+    e[E_BASE] = base;
+    e[E_COUNT] = m_tiles;
+    e[E_FULL] = m_full;
+    e[E_LAST] = m_last;
+    *reinterpret_cast<int64_t*>(e + E_LINE) =
+        static_cast<int64_t>(line_upto - on_line) -
+        static_cast<int64_t>(skipped);
+  }
+  if (r == 0) {
+    work[H_MODE] = kModeTile;
+    work[H_ACTIVE] = s_act;
+    work[H_TOTAL] = U;
+    work[H_CTAS] = G;
+    work[H_WAVES] = K;
+  }
+}
 
 // The attention's work list, by one CTA.  ql and kv are stream threadIdx.x's
-// rows and keys.
+// rows and keys, q0 its first packed row.
 __device__ void build_work(const PlanArgs& a, int ql, int kv, int q0,
-                           int chunk, int window, uint64_t* red, int* s_a, int* s_b,
-                           int* s_c, int64_t* s_cost) {
-  const wan_paged_t& c = a.c;
-  const int r = threadIdx.x;
-  int32_t* work = c.work;
-  const bool on = ql > 0;
-  const int lo = on ? key_lo(kv - ql, chunk, window) : 0;
+                           int chunk, int window, uint64_t* red,
+                           const WorkMem& mem) {
+  const int lo = ql > 0 ? key_lo(kv - ql, chunk, window) : 0;
   if (a.few) {
-    // 64-key stages from the first row's first key to the end; at least one,
-    // so that rows that see nothing are written too
-    int n = 0;
-    if (on) n = (kv + kStage - 1) / kStage - min(lo, kv - 1) / kStage;
-    const uint64_t sc = block_scan(
-        (static_cast<uint64_t>(on) << 40) | static_cast<uint64_t>(n), red);
-    const int idx = static_cast<int>(sc >> 40) - on;
-    const int base = static_cast<int>(sc & 0xFFFFFFFFFFull) - n;
-    if (on) {
-      int32_t* e = work + kHdr + kEnt * idx;
-      e[E_STREAM] = r;
-      e[E_BASE] = base;
-      e[E_COUNT] = n;
-      e[E_STAGE0] = min(lo, kv - 1) / kStage;
-      e[E_KV] = kv;
-      e[E_ROWS] = ql;
-      e[E_Q0] = q0;
-    }
-    if (r == blockDim.x - 1) {
-      const int64_t total = static_cast<int64_t>(base + n) * c.kv_heads;
-      const int64_t most = static_cast<int64_t>(a.sms) * kFewCtasPerSm;
-      int64_t ctas = total / kMinStages;
-      ctas = ctas < 1 ? 1 : ctas > most ? most : ctas;
-      work[H_MODE] = kModeFew;
-      work[H_ACTIVE] = idx + on;
-      work[H_TOTAL] = static_cast<int>(total);
-      work[H_CTAS] = static_cast<int>(ctas);
-      work[H_ROWS] = 0;
-    }
+    build_few(a, ql, kv, q0, lo, red);
     return;
   }
   // 128-key blocks of the longest tile (an upper bound under a window)
   int nb = 0;
-  if (on) {
-    nb = (kv + kBlock - 1) / kBlock - min(lo, kv - 1) / kBlock;
-    if (nb < 1) nb = 1;
-  }
-  // streams by falling length: CTA i takes units i, i + G, ... so its share
-  // is heaviest for i = 0 and within one unit of the lightest.  Keys hold
-  // the length (capped, which only changes the order) over the place; a
-  // bitonic network of shuffles and, across warps, shared memory sorts them.
-  const int n_act = __syncthreads_count(on);
-  const int tiles = (ql + kTileRows - 1) / kTileRows;
-  uint32_t key = on ? (static_cast<uint32_t>(min(nb, (1 << 22) - 1)) << 10) |
-                          static_cast<uint32_t>(kMaxStreams - 1 - r)
-                    : 0u;
-  uint32_t* s_key = reinterpret_cast<uint32_t*>(s_a);
-  if (c.n_streams > 1) {
-    for (int k = 2; k <= kMaxStreams; k <<= 1) {
-      for (int j = k >> 1; j > 0; j >>= 1) {
-        uint32_t other;
-        if (j >= 32) {
-          __syncthreads();
-          s_key[r] = key;
-          __syncthreads();
-          other = s_key[r ^ j];
-        } else {
-          other = __shfl_xor_sync(0xffffffffu, key, j);
-        }
-        // falling order where bit k of r is clear
-        const bool keep_max = ((r & k) == 0) == ((r & j) == 0);
-        key = keep_max ? max(key, other) : min(key, other);
-      }
-    }
-  }
-  const int src = kMaxStreams - 1 - static_cast<int>(key & (kMaxStreams - 1));
-  // stream src is the r-th longest
-  __syncthreads();
-  s_a[r] = nb;
-  s_b[r] = tiles;
-  s_c[r] = ql;
-  __syncthreads();
-  const bool mine = r < n_act;
-  const int m_nb = mine ? s_a[src] : 0;
-  const int m_tiles = mine ? s_b[src] : 0;
-  const int m_ql = mine ? s_c[src] : 0;
-  __syncthreads();
-  s_a[r] = m_nb;
-  s_b[r] = m_tiles;
-  const int64_t whole = static_cast<int64_t>(block_scan(
-      static_cast<uint64_t>(m_tiles) * c.heads, red));
-  __shared__ int s_many;
-  if (r == blockDim.x - 1) s_many = whole >= kManyWaves * a.sms;
-  __syncthreads();
-  // warp w tries ranges of at most 1 / (w + 1) of the longest stream; with
-  // many waves of units there is nothing to gain
-  const int lane = r & 31, w = r >> 5;
-  const int longest = n_act ? s_a[0] : 0;
-  const int range = (longest + w) / (w + 1);
-  int64_t cost = INT64_MAX;
-  if (n_act && (w == 0 || (range >= kMinRange && !s_many))) {
-    int64_t t = 0, base = 0, slots = 0;
-    for (int i0 = 0; i0 < n_act && !(s_many && w == 0); i0 += 32) {
-      const int i = i0 + lane;
-      int64_t units = 0;
-      int len = 0, ns = 1;
-      if (i < n_act) {
-        ns = (s_a[i] + range - 1) / range;
-        units = static_cast<int64_t>(s_b[i]) * c.heads * ns;
-        len = (s_a[i] + ns - 1) / ns;
-      }
-      int64_t incl = units;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t u = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += u;
-      }
-      // units of CTA 0 among p0 .. p1 - 1 (capped: a list that long is one
-      // of whole units, whose cost is not compared)
-      const uint32_t p1 =
-          static_cast<uint32_t>(min(base + incl, static_cast<int64_t>(1) << 30));
-      const uint32_t p0 = static_cast<uint32_t>(
-          min(base + incl - units, static_cast<int64_t>(1) << 30));
-      const uint32_t cnt = (p1 + a.sms - 1) / a.sms - (p0 + a.sms - 1) / a.sms;
-      t += static_cast<int64_t>(cnt) * (len + kUnitCost);
-      if (ns > 1) slots += units;
-      base += __shfl_sync(0xffffffffu, incl, 31);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      t += __shfl_xor_sync(0xffffffffu, t, o);
-      slots += __shfl_xor_sync(0xffffffffu, slots, o);
-    }
-    if (slots <= static_cast<int64_t>(a.sms) * kTileSlotsPerSm)
-      cost = kSlotsPerBlock * t + (slots ? kSlotsPerBlock * kJoinCost : 0) +
-             slots;
-  }
-  if (lane == 0) s_cost[w] = cost;
-  __syncthreads();
-  int64_t low = s_cost[lane];
-  int best = lane;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const int64_t lo2 = __shfl_xor_sync(0xffffffffu, low, o);
-    const int b2 = __shfl_xor_sync(0xffffffffu, best, o);
-    if (lo2 < low || (lo2 == low && b2 < best)) {
-      low = lo2;
-      best = b2;
-    }
-  }
-  const int rng = max((longest + best) / (best + 1), 1);
-  // entry r of the list
-  const int ns = mine ? (m_nb + rng - 1) / rng : 1;
-  const uint64_t units = static_cast<uint64_t>(m_tiles) * c.heads * ns;
-  const uint64_t slots = ns > 1 ? units : 0;
-  const uint64_t rows = ns > 1 ? static_cast<uint64_t>(m_ql) * c.heads : 0;
-  const uint64_t su = block_scan((units << 32) | slots, red);
-  const uint64_t sr = block_scan(rows, red);
-  if (mine) {
-    int32_t* e = work + kHdr + kEnt * r;
-    e[E_STREAM] = src;
-    e[E_BASE] = static_cast<int>((su >> 32) - units);
-    e[E_COUNT] = m_tiles;
-    e[E_SPLIT] = ns;
-    e[E_SLOT] = static_cast<int>((su & 0xFFFFFFFFull) - slots);
-    e[E_ROW] = static_cast<int>(sr - rows);
-  }
-  if (r == blockDim.x - 1) {
-    work[H_MODE] = kModeTile;
-    work[H_ACTIVE] = n_act;
-    work[H_TOTAL] = static_cast<int>(su >> 32);
-    work[H_CTAS] = a.sms;
-    work[H_ROWS] = static_cast<int>(sr);
-  }
+  if (ql > 0)
+    nb = max((kv + kBlock - 1) / kBlock - min(lo, kv - 1) / kBlock, 1);
+  build_tiles(a, ql, nb, red, mem);
 }
 
 __global__ void __launch_bounds__(kPlanThreads)
     paged_plan_kernel(const __grid_constant__ PlanArgs a) {
   __shared__ uint64_t red[32];
-  __shared__ int64_t s_cost[32];
   __shared__ int s_end[kMaxStreams];    // packed rows up to and with stream r
   __shared__ int s_rows[kMaxStreams];   // admitted rows
   __shared__ int s_back[kMaxStreams];   // pages coming back, inclusive
   __shared__ int s_need[kMaxStreams];   // pages going out, inclusive
   __shared__ int s_old[kMaxStreams];    // tokens before the step
   __shared__ int s_from[kMaxStreams];   // first page coming back
-  __shared__ int s_hw[kMaxStreams];     // tokens of a frame and of a row,
-  __shared__ int s_w[kMaxStreams];      //   with their div_magic
+  // tokens of a frame and of a row, with their div_magic
+  __shared__ __align__(8) int s_dims[2 * kMaxStreams];
+  int* s_hw = s_dims;
+  int* s_w = s_dims + kMaxStreams;
   __shared__ uint32_t s_mhw[kMaxStreams];
   __shared__ uint32_t s_mw[kMaxStreams];
   const wan_paged_t& c = a.c;
@@ -417,7 +462,8 @@ __global__ void __launch_bounds__(kPlanThreads)
   if (ctas > 1) cluster_arrive();
   if (rank == movers) {
     build_work(a, admit ? rows : 0, kv, r ? s_end[r - 1] : 0, cfg.z, cfg.w,
-               red, s_back, s_need, s_from, s_cost);
+               red, WorkMem{s_back, s_need, s_from, s_rows,
+                            reinterpret_cast<unsigned long long*>(s_dims)});
     __syncthreads();
     cluster_wait();
     return;
@@ -488,7 +534,8 @@ __global__ void __launch_bounds__(kPlanThreads)
   if (ctas == 1) {
     __syncthreads();
     build_work(a, admit ? rows : 0, kv, r ? s_end[r - 1] : 0, cfg.z, cfg.w,
-               red, s_back, s_need, s_from, s_cost);
+               red, WorkMem{s_back, s_need, s_from, s_rows,
+                            reinterpret_cast<unsigned long long*>(s_dims)});
   }
 }
 
@@ -502,7 +549,8 @@ __global__ void __launch_bounds__(kPlanThreads)
 // is read twice (the second time from L2).  One item a warp and as many CTAs
 // as that takes: new CTAs load while others store, where a warp that walked
 // several items alternated between the two (43,200 rows x 40 heads, 2.65 GB:
-// 446 us walking, 414 us so, 6.4 TB/s; 3 CTAs an SM instead of 4: 499 us).
+// 446 us walking, 414 us so, 6.4 TB/s; 3 CTAs an SM instead of 4: 499 us;
+// 4,680 rows x 12 heads: 14.5 us at 7 CTAs an SM, 15.8 at 6).
 constexpr int kWrThreads = 128;
 constexpr int kWrWarps = kWrThreads / 32;
 constexpr int kWrMaxRows = 20;
@@ -523,7 +571,7 @@ struct WriteArgs {
 
 template <int kRows>
 constexpr int wr_min_blocks() {
-  return kRows <= 4 ? 8 : kRows <= 8 ? 6 : kRows <= 12 ? 5 : 4;
+  return kRows <= 4 ? 9 : kRows <= 8 ? 7 : kRows <= 12 ? 6 : 4;
 }
 
 // kRows 0: any head count, two passes over the row.
@@ -627,6 +675,38 @@ int page_shift_of(int page_size) {
   return s;
 }
 
+// 16 if a cluster of 16 plan CTAs can be resident on the device, else 8.
+unsigned big_cluster(int dev) {
+  static std::mutex mu;
+  static unsigned size[64];
+  if (dev < 0 || dev >= 64) return 8;
+  std::lock_guard<std::mutex> lock(mu);
+  if (size[dev] == 0) {
+    size[dev] = 8;
+    if (cudaFuncSetAttribute(paged_plan_kernel,
+                             cudaFuncAttributeNonPortableClusterSizeAllowed,
+                             1) == cudaSuccess) {
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3(16);
+      cfg.blockDim = dim3(kPlanThreads);
+      cudaLaunchAttribute at[1];
+      at[0].id = cudaLaunchAttributeClusterDimension;
+      at[0].val.clusterDim.x = 16;
+      at[0].val.clusterDim.y = 1;
+      at[0].val.clusterDim.z = 1;
+      cfg.attrs = at;
+      cfg.numAttrs = 1;
+      int n = 0;
+      if (cudaOccupancyMaxActiveClusters(&n, paged_plan_kernel, &cfg) ==
+              cudaSuccess &&
+          n > 0)
+        size[dev] = 16;
+    }
+    cudaGetLastError();
+  }
+  return size[dev];
+}
+
 int device_sms(int dev) {
   int n = 0;
   if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) !=
@@ -653,7 +733,6 @@ int wan_paged_plan(const wan_paged_t* c, const int32_t* new_lens, void* s) {
   int st = check_cache(c);
   if (st != WAN_OK) return st;
   if (!new_lens) return WAN_EINVAL;
-  if (!aligned16(new_lens)) return WAN_EALIGN;
   int dev = 0;
   if ((st = check_device(&dev)) != WAN_OK) return st;
   PlanArgs a;
@@ -661,12 +740,16 @@ int wan_paged_plan(const wan_paged_t* c, const int32_t* new_lens, void* s) {
   a.new_lens = new_lens;
   a.page_shift = page_shift_of(c->page_size);
   a.sms = device_sms(dev);
-  if (a.sms < 1) return WAN_ECUDA;
+  if (a.sms < 1 || a.sms * kFewCtasPerSm > kMaxCtas) return WAN_ECUDA;
   a.few = few_mode(c) ? 1 : 0;
   cudaLaunchConfig_t cfg = {};
-  // One CTA up to 2,048 records (two a thread); the portable cluster of 8
-  // beyond, where the records' writes take over.
-  const unsigned ctas = c->token_cap <= 2 * kPlanThreads ? 1 : 8;
+  // One CTA up to 2,048 records (two a thread), a cluster of 8 up to 32,768,
+  // of 16 beyond where the device can run one (114,041 records of 48
+  // streams: 13.4 us with 16, 18.7 with 8; 4,685 records: 9.7 us with 8, 13.2
+  // with one CTA).
+  const unsigned ctas = c->token_cap <= 2 * kPlanThreads    ? 1
+                        : c->token_cap <= 32 * kPlanThreads ? 8
+                                                            : big_cluster(dev);
   cfg.gridDim = dim3(ctas);
   cfg.blockDim = dim3(kPlanThreads);
   cfg.stream = as_stream(s);

@@ -17,36 +17,50 @@ constexpr int kFewRows = 16;
 constexpr int kModeNone = 0, kModeFew = 1, kModeTile = 2;
 
 // kFew: the (stream, key head, 64-key stage) items form one line that is cut
-// into equal parts, one per CTA.  kTile: units of (256-row tile, head, key
-// range); a stream's 128-key blocks are cut into nsplit ranges.
+// into equal parts, one per CTA.
+// kTile: units are (256-row tile pair, head), numbered streams by falling
+// length, then head, then tile pair (the stream's last one first: it sees the
+// most keys).  H_WAVES rounds of one whole unit per CTA come first, in turn
+// up and down the CTAs; the units behind them form a line of their weights
+// that is cut so that all CTAs end together (LINE[c] .. LINE[c + 1] for CTA
+// c), inside a unit's keys where it falls there.
 constexpr int kStage = 64;
 constexpr int kBlock = 128;
 constexpr int kTileRows = 256;
 constexpr int kFewCtasPerSm = 2;
-constexpr int kTileSlotsPerSm = 4;
+constexpr int kMaxCtas = 1023;
 
-// work[0 .. kHdr): header; then kEnt ints per active stream.
-constexpr int kHdr = 16;
+// Weight of a unit: 8 a 128-key block with two row tiles, 5 with one, and
+// kUnitWeight for its start and end (measured: see build_tiles).
+constexpr int kPairWeight = 8;
+constexpr int kOneWeight = 5;
+constexpr int kUnitWeight = 24;
+
+// work: a header, LINE[0 .. kMaxCtas], then kEnt ints per active stream.
+constexpr int kLine = 16;
+constexpr int kHdr = kLine + kMaxCtas + 1;
 constexpr int kEnt = 8;
 enum : int {
   H_MODE = 0,     // kMode*
   H_ACTIVE = 1,   // entries
   H_TOTAL = 2,    // kFew: stages x key heads; kTile: units
-  H_CTAS = 3,     // kFew: CTAs that share the line
-  H_ROWS = 4      // kTile: (row, head) pairs of split streams
+  H_CTAS = 3,     // CTAs that take part
+  H_WAVES = 4     // kTile: rounds of whole units
 };
 enum : int {
   E_STREAM = 0,
   E_BASE = 1,     // kFew: stages before it; kTile: units before it
-  E_COUNT = 2,    // kFew: its stages; kTile: its 256-row tiles
-  E_SPLIT = 3,    // kTile: key ranges
-  E_SLOT = 4,     // kTile: first partial-result slot (nsplit > 1)
-  E_ROW = 5,      // kTile: split (row, head) pairs before it
+  E_COUNT = 2,    // kFew: its stages; kTile: its tile pairs
   // kFew: what a CTA needs to start fetching, in one 32-byte read
   E_STAGE0 = 3,   // first stage
   E_KV = 4,       // tokens of the stream
   E_ROWS = 5,     // its new tokens
-  E_Q0 = 6        // their first packed row
+  E_Q0 = 6,       // their first packed row
+  // kTile
+  E_FULL = 3,     // weight of a unit with two row tiles
+  E_LAST = 4,     // weight of a unit of the last tile pair
+  E_LINE = 6      // (64 bits) the line's place at which the stream's units
+                  // would start, had all of them been on it
 };
 
 // kFew: CTA c of `ctas` takes places [first(c), first(c + 1)) of the line of

@@ -80,17 +80,17 @@ __device__ __forceinline__ void launch_dependents() {
 struct JoinAcc {
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   float m = -INFINITY, l = 0.f;
-  // Parts 0 .. n - 1, part k at row_of(k) of the workspace.  32 parts at a
-  // time: their maxima and sums come with one load a lane, their O rows with
+  // Parts 0 .. n - 1 (those that has(k) says were written), part k at
+  // row_of(k) of the workspace.  32 parts at a time: their maxima and sums come with one load a lane, their O rows with
   // batches of independent loads (loads under a condition ran one after the
   // other: 25 parts took 13 us instead of 4).
   static constexpr int kBatch = 16;
-  template <typename RowOf>
-  __device__ __forceinline__ void add_all(int n, int lane,
-                                          const PagedArgs& a, RowOf row_of) {
+  template <typename RowOf, typename Has>
+  __device__ __forceinline__ void add_all(int n, int lane, const PagedArgs& a,
+                                          RowOf row_of, Has has) {
     for (int k0 = 0; k0 < n; k0 += 32) {
       float2 ml = make_float2(-INFINITY, 0.f);
-      if (k0 + lane < n) ml = a.part_ml[row_of(k0 + lane)];
+      if (k0 + lane < n && has(k0 + lane)) ml = a.part_ml[row_of(k0 + lane)];
       // a part that saw no key has no O
       if (!(ml.y > 0.f)) ml = make_float2(-INFINITY, 0.f);
       float top = ml.x;
@@ -573,7 +573,7 @@ __global__ void __launch_bounds__(128)
     const bool mid = xs > line.first(c0);
     acc.add_all(c1 - c0 + 1, lane, args, [&](int k) {
       return (2ll * (c0 + k) + (k == 0 && mid ? 1 : 0)) * kRows + r;
-    });
+    }, [](int) { return true; });
     acc.write(args.o + ((static_cast<int64_t>(q0) + i) * args.c.heads +
                         head * args.group + (r - i * args.group)) * HD,
               lane);
@@ -587,10 +587,10 @@ __global__ void __launch_bounds__(128)
 // memory and softmax) fed from pages: a 128-key block is 2 to 8 TMA boxes
 // per 64-channel half, one lane of the producer warp per box, the block
 // table entry of the next block fetched while this one loads.  One
-// persistent CTA per SM walks units u = blockIdx.x, + gridDim.x, ... of the
-// plan's list: (256 rows of a stream, head, range of its key blocks), tiles
-// fastest so that neighbours read the same keys at the same time, streams by
-// falling length.  A unit whose rows fit one tile runs that tile alone.
+// persistent CTA per SM walks its share of the plan's division: rounds of
+// whole units (256 rows of a stream, head), then its part of the line of the
+// last units, so that all CTAs end together whatever the streams' lengths.
+// A unit whose rows fit one tile runs that tile alone.
 // Output rows are staged in the tile's own Q buffer (free once the unit's
 // last P V is done) and stored 512 contiguous bytes a warp instruction with
 // a row check, since a stream's last tile ends inside the next stream's rows
@@ -611,6 +611,12 @@ enum : int {
   NBAR
 };
 
+// Where a CTA is in its share of the work: whole unit k while k < waves,
+// then place x of the line.
+struct Walk {
+  int k, x;
+};
+
 struct Unit {
   int stream, head;
   int q0;            // packed row of the tile pair's first row
@@ -618,22 +624,104 @@ struct Unit {
   int a0;            // their first position
   int kv, chunk, window;
   int lo, hi;        // keys that any of the rows sees
-  int kb0, nblk;     // key blocks of the unit's range (may be none)
-  int slot;          // partial-result slot, -1: the keys in full
+  int kb0, nblk;     // key blocks of the part (may be none)
+  int slot;          // partial-result slot, -1: the unit's keys in full
+  int span;          // places of the line
 };
 
-__device__ __forceinline__ Unit unit_at(const PagedArgs& a, int u) {
-  Unit t;
-  const int32_t* e = find_entry(a.c.work, pg::E_BASE, 1, u);
+__device__ __forceinline__ Walk walk_begin(const PagedArgs& a) {
+  Walk w;
+  w.k = 0;
+  w.x = __ldg(a.c.work + pg::kLine + blockIdx.x);
+  return w;
+}
+
+__device__ __forceinline__ void walk_next(const PagedArgs& a, Walk& w,
+                                          int span) {
+  if (w.k < __ldg(a.c.work + pg::H_WAVES))
+    ++w.k;
+  else
+    w.x += span;
+}
+
+// Key blocks of a unit's nb before place s of its `weight` places.
+__device__ __forceinline__ int cut(int nb, int s, int weight) {
+  return static_cast<int>(static_cast<int64_t>(nb) * s / weight);
+}
+
+// Weight of a stream's units before its unit `n` (the last tile pair, which
+// may be lighter, is the first unit of each head).
+__device__ __forceinline__ int64_t weight_before(int n, int tiles, int full,
+                                                 int last) {
+  const int rag = (n + tiles - 1) / tiles;
+  return static_cast<int64_t>(n - rag) * full +
+         static_cast<int64_t>(rag) * last;
+}
+
+// The part at w; false at the end of the CTA's share.
+__device__ __forceinline__ bool unit_at(const PagedArgs& a, const Walk& w,
+                                        Unit& t) {
+  const int32_t* work = a.c.work;
+  const int32_t* e;
+  int local, s0 = 0, s1 = 1, weight = 1;
+  t.slot = -1;
+  t.span = 0;
+  if (w.k < __ldg(work + pg::H_WAVES)) {
+    const int ctas = __ldg(work + pg::H_CTAS);
+    const int c = blockIdx.x;
+    const int u = w.k * ctas + (w.k & 1 ? ctas - 1 - c : c);
+    e = find_entry(work, pg::E_BASE, 1, u);
+    local = u - __ldg(e + pg::E_BASE);
+  } else {
+    const int x0 = __ldg(work + pg::kLine + blockIdx.x);
+    const int x1 = __ldg(work + pg::kLine + blockIdx.x + 1);
+    if (w.x >= x1) return false;
+    // the stream whose units hold place x, and the place among them
+    const int32_t* base = work + pg::kHdr;
+    int lo = 0, hi = __ldg(work + pg::H_ACTIVE) - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      const int32_t* m = base + pg::kEnt * mid;
+      const int64_t line =
+          __ldg(reinterpret_cast<const long long*>(m + pg::E_LINE));
+      // a stream's first place: units of earlier rounds are not on the line
+      const int skip = min(max(__ldg(work + pg::H_WAVES) *
+                                       __ldg(work + pg::H_CTAS) -
+                                   __ldg(m + pg::E_BASE),
+                               0),
+                           __ldg(m + pg::E_COUNT) * a.c.heads);
+      if (line + weight_before(skip, __ldg(m + pg::E_COUNT),
+                               __ldg(m + pg::E_FULL),
+                               __ldg(m + pg::E_LAST)) <= w.x)
+        lo = mid;
+      else
+        hi = mid - 1;
+    }
+    e = base + pg::kEnt * lo;
+    const int tiles = __ldg(e + pg::E_COUNT);
+    const int full = __ldg(e + pg::E_FULL), last = __ldg(e + pg::E_LAST);
+    const int64_t y =
+        w.x - __ldg(reinterpret_cast<const long long*>(e + pg::E_LINE));
+    const int64_t period = static_cast<int64_t>(tiles - 1) * full + last;
+    const int head = static_cast<int>(y / period);
+    const int rest = static_cast<int>(y - head * period);
+    int tile = 0, off = rest;
+    weight = last;
+    if (rest >= last) {
+      tile = 1 + (rest - last) / full;
+      off = (rest - last) % full;
+      weight = full;
+    }
+    local = head * tiles + tile;
+    t.span = min(weight - off, x1 - w.x);
+    s0 = off;
+    s1 = off + t.span;
+    if (t.span < weight) t.slot = 2 * blockIdx.x + (w.x == x0 ? 0 : 1);
+  }
   t.stream = __ldg(e + pg::E_STREAM);
   const int tiles = __ldg(e + pg::E_COUNT);
-  const int ns = __ldg(e + pg::E_SPLIT);
-  const int local = u - __ldg(e + pg::E_BASE);
-  const int rest = local / tiles;
-  const int tx = tiles - 1 - (local - rest * tiles);  // longest keys first
-  t.head = rest / ns;
-  const int split = rest - t.head * ns;
-  t.slot = ns > 1 ? __ldg(e + pg::E_SLOT) + local : -1;
+  t.head = local / tiles;
+  const int tx = tiles - 1 - (local - t.head * tiles);
   const int ql = __ldg(a.c.q_lens + t.stream);
   t.kv = keys_of(a, t.stream);
   const int4 cfg = __ldg(reinterpret_cast<const int4*>(a.c.streams) + t.stream);
@@ -646,9 +734,9 @@ __device__ __forceinline__ Unit unit_at(const PagedArgs& a, int u) {
   t.hi = pg::key_hi(t.a0 + t.rows - 1, t.chunk, t.kv);
   const int b0 = t.lo / BN;
   const int nb = max((t.hi + BN - 1) / BN - b0, 0);
-  t.kb0 = b0 + split * nb / ns;
-  t.nblk = t.rows > 0 ? b0 + (split + 1) * nb / ns - t.kb0 : 0;
-  return t;
+  t.kb0 = b0 + cut(nb, s0, weight);
+  t.nblk = t.rows > 0 ? b0 + cut(nb, s1, weight) - t.kb0 : 0;
+  return true;
 }
 
 __global__ void __launch_bounds__(wan::kThreads, 1)
@@ -662,10 +750,11 @@ __global__ void __launch_bounds__(wan::kThreads, 1)
   __shared__ int s_abort;
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  const int units = __ldg(args.c.work + pg::H_MODE) == pg::kModeTile
-                        ? __ldg(args.c.work + pg::H_TOTAL)
-                        : 0;
-  if (static_cast<int>(blockIdx.x) >= units) return;
+  if (__ldg(args.c.work + pg::H_MODE) != pg::kModeTile ||
+      static_cast<int>(blockIdx.x) >= __ldg(args.c.work + pg::H_CTAS) ||
+      __ldg(args.c.work + pg::H_TOTAL) < 1)
+    return;
+  launch_dependents();
   volatile int* abort_flag = &s_abort;
   int* status = &g_wan_status;
   const uint32_t raw = smem_u32(smem_raw);
@@ -715,8 +804,9 @@ __global__ void __launch_bounds__(wan::kThreads, 1)
       const int row0 = lane << args.box_shift;  // this lane's box
       bool ok = true;
       int nq = 0, nq1 = 0, nk = 0, nv = 0;  // units, with a 2nd tile; blocks
-      for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
-        const Unit c = unit_at(args, u);
+      Unit c;
+      for (Walk w = walk_begin(args); ok && unit_at(args, w, c);) {
+        walk_next(args, w, c.span);
         if (c.nblk == 0) continue;
         const bool two = c.rows > BM;
         int64_t pos = static_cast<int64_t>(c.kb0) * BN + row0;
@@ -849,8 +939,9 @@ __global__ void __launch_bounds__(wan::kThreads, 1)
       bool ok = true;
       int g0 = 0, h0 = 0;  // blocks of earlier units: all, with a 2nd tile
       int n0 = 0, n1 = 0;  // units before this one, with a 2nd tile
-      for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
-        const Unit c = unit_at(args, u);
+      Unit c;
+      for (Walk w = walk_begin(args); ok && unit_at(args, w, c);) {
+        walk_next(args, w, c.span);
         if (c.nblk == 0) continue;
         const bool two = c.rows > BM;
         ok = wait_warp(&bar[QFULL], n0 & 1, abort_flag, status);
@@ -909,32 +1000,35 @@ __global__ void __launch_bounds__(wan::kThreads, 1)
     const uint32_t o_col = lane_base + TM_O + t * 128;
     const float c2 = args.scale_log2;
     bool ok = true;
-    int gt = 0, nt = 0;  // this tile's blocks and units so far
-    for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
-      int kb0, nblk, row_lo = 0, row_hi = INT32_MAX;
+    uint32_t sph = 0, uph = 0;  // phases of this tile's scores and units
+    for (Walk w = walk_begin(args); ok;) {
+      int nblk, span, lim_lo = 0, lim_hi = INT32_MAX;
       {
-        const Unit c = unit_at(args, u);
-        kb0 = c.kb0;
+        Unit c;
+        if (!unit_at(args, w, c)) break;
+        span = c.span;
         nblk = c.nblk;
+        // rows behind the tile's last take part unmasked, never written
         if (t * BM + r < c.rows) {
           const int a = c.a0 + t * BM + r;
-          row_lo = pg::key_lo(max(a, 0), c.chunk, c.window);
-          row_hi = pg::key_hi(a, c.chunk, c.kv);
+          lim_lo = pg::key_lo(max(a, 0), c.chunk, c.window) - c.kb0 * BN;
+          lim_hi = pg::key_hi(a, c.chunk, c.kv) - c.kb0 * BN;
         }
-        // rows behind the tile's last take part unmasked, never written
-        if (t * BM >= c.rows) continue;  // a unit of one tile
+        if (t * BM >= c.rows) {  // a unit of one tile
+          walk_next(args, w, span);
+          continue;
+        }
       }
       float m_run = -INFINITY;
       float l_run = 0.f;
       for (int j = 0; j < nblk; ++j) {
-        ok = wait_warp(&bar[SFULL + t], (gt + j) & 1, abort_flag, status);
+        ok = wait_warp(&bar[SFULL + t], sph, abort_flag, status);
         if (!ok) break;
+        sph ^= 1;
         tc_fence_after();
         float s[BN];
         tmem_ld128(s_col, s);
         tmem_ld_wait128(s);
-        const int key0 = (kb0 + j) * BN;
-        const int lim_lo = row_lo - key0, lim_hi = row_hi - key0;
         const bool masked =
             __any_sync(0xffffffffu, lim_hi < BN || lim_lo > 0);
         if (masked) {
@@ -942,6 +1036,8 @@ __global__ void __launch_bounds__(wan::kThreads, 1)
           for (int c = 0; c < BN; ++c)
             if (c >= lim_hi || c < lim_lo) s[c] = -INFINITY;
         }
+        lim_lo -= BN;
+        lim_hi -= BN;
         const float mx = (masked ? rowmax_masked<BN>(s) : rowmax<BN>(s)) * c2;
         if (j == 0) {
           m_run = mx;
@@ -986,16 +1082,17 @@ __global__ void __launch_bounds__(wan::kThreads, 1)
         l_run += tsum.x + tsum.y;
       }
       if (!ok) break;
-      gt += nblk;
       if (nblk > 0) {
-        ok = wait_warp(&bar[OFINAL + t], nt & 1, abort_flag, status);
+        ok = wait_warp(&bar[OFINAL + t], uph, abort_flag, status);
         if (!ok) break;
+        uph ^= 1;
         tc_fence_after();
       }
       // Coordinates again instead of holding them through the key loop.
-      int u_e = u;
-      asm volatile("" : "+r"(u_e));
-      const Unit ce = unit_at(args, u_e);
+      asm volatile("" : "+r"(w.k), "+r"(w.x));
+      Unit ce;
+      unit_at(args, w, ce);
+      walk_next(args, w, ce.span);
       const int wrow0 = (warp & 3) * 32;  // this warp's rows of the tile
       const int live = min(ce.rows - t * BM - wrow0,
                            args.c.token_cap - ce.q0 - t * BM - wrow0);
@@ -1080,7 +1177,6 @@ __global__ void __launch_bounds__(wan::kThreads, 1)
       if (nblk > 0) {
         // O is read and the staging rows too: the next unit's first P V and
         // Q load may overwrite them
-        ++nt;
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
@@ -1096,32 +1192,66 @@ __global__ void __launch_bounds__(wan::kThreads, 1)
   }
 }
 
-// One warp per (row, head) of the streams whose keys were split.
+// One warp per row of the line's units that several CTAs shared.
 __global__ void __launch_bounds__(128)
     paged_tile_join(const __grid_constant__ PagedArgs args) {
   const int32_t* work = args.c.work;
-  if (work[pg::H_MODE] != pg::kModeTile) return;
-  const int total = work[pg::H_ROWS];
+  if (__ldg(work + pg::H_MODE) != pg::kModeTile) return;
+  const int ctas = __ldg(work + pg::H_CTAS);
+  const int first = __ldg(work + pg::H_WAVES) * ctas;
+  const int n = __ldg(work + pg::H_TOTAL) - first;  // units on the line
+  const int32_t* line = work + pg::kLine;
   const int lane = threadIdx.x & 31;
-  const int64_t warps = static_cast<int64_t>(gridDim.x) * 4;
+  const int warps = gridDim.x * 4;
   const int heads = args.c.heads;
   grid_dependency_wait();
-  for (int64_t it = blockIdx.x * 4ll + (threadIdx.x >> 5); it < total;
-       it += warps) {
-    const int32_t* e = find_entry(work, pg::E_ROW, 1, it);
-    const int stream = e[pg::E_STREAM];
-    const int tiles = e[pg::E_COUNT], ns = e[pg::E_SPLIT];
-    const int local = static_cast<int>(it) - e[pg::E_ROW];
-    const int i = local / heads, head = local - i * heads;
-    const int64_t row = static_cast<int64_t>(args.c.q_start[stream]) + i;
-    if (row >= args.c.token_cap) continue;
-    const int tx = tiles - 1 - i / pg::kTileRows;
+  for (int it = blockIdx.x * 4 + (threadIdx.x >> 5);
+       it < n * pg::kTileRows; it += warps) {
+    const int u = first + it / pg::kTileRows;
+    const int i = it % pg::kTileRows;
+    const int32_t* e = find_entry(work, pg::E_BASE, 1, u);
+    const int tiles = __ldg(e + pg::E_COUNT);
+    const int full = __ldg(e + pg::E_FULL), last = __ldg(e + pg::E_LAST);
+    const int local = u - __ldg(e + pg::E_BASE);
+    const int head = local / tiles;
+    const int tile = local - head * tiles;
+    const int x0 = static_cast<int>(
+        __ldg(reinterpret_cast<const long long*>(e + pg::E_LINE)) +
+        weight_before(local, tiles, full, last));
+    const int x1 = x0 + (tile == 0 ? last : full) - 1;
+    // CTAs that hold its first and its last place
+    auto holder = [&](int x) {
+      int lo = 0, hi = ctas - 1;
+      while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (__ldg(line + mid + 1) > x)
+          hi = mid;
+        else
+          lo = mid + 1;
+      }
+      return lo;
+    };
+    const int c0 = holder(x0), c1 = holder(x1);
+    if (c0 == c1) continue;
+    const int stream = __ldg(e + pg::E_STREAM);
+    const int tx = tiles - 1 - tile;
+    const int row = tx * pg::kTileRows + i;
+    const int64_t at = static_cast<int64_t>(__ldg(args.c.q_start + stream)) +
+                       row;
+    if (row >= __ldg(args.c.q_lens + stream) || at >= args.c.token_cap)
+      continue;
+    // the first CTA's part is its last one unless the unit starts its share
+    const bool mid = x0 > __ldg(line + c0);
     JoinAcc acc;
-    const int64_t slot0 = e[pg::E_SLOT] + head * ns * tiles + tx;
-    acc.add_all(ns, lane, args, [&](int k) {
-      return (slot0 + k * tiles) * pg::kTileRows + i % pg::kTileRows;
-    });
-    acc.write(args.o + (row * heads + head) * HD, lane);
+    acc.add_all(
+        c1 - c0 + 1, lane, args,
+        [&](int k) {
+          return (2ll * (c0 + k) + (k == 0 && mid ? 1 : 0)) * pg::kTileRows +
+                 i;
+        },
+        // a CTA between them may have no share of the line
+        [&](int k) { return __ldg(line + c0 + k) < __ldg(line + c0 + k + 1); });
+    acc.write(args.o + (at * heads + head) * HD, lane);
   }
 }
 }  // namespace tile
@@ -1143,8 +1273,7 @@ int paged_sms() {
 
 // Partial-result slots of the device and rows of one slot.
 int64_t paged_slots(const wan_paged_t* c, int sms) {
-  return pg::few_mode(c) ? 2ll * pg::kFewCtasPerSm * sms
-                         : static_cast<int64_t>(pg::kTileSlotsPerSm) * sms;
+  return pg::few_mode(c) ? 2ll * pg::kFewCtasPerSm * sms : 2ll * sms;
 }
 int paged_slot_rows(const wan_paged_t* c) {
   return pg::few_mode(c) ? pg::kFewRows : pg::kTileRows;

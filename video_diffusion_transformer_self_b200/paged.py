@@ -25,6 +25,7 @@ from . import wan
 
 
 _SCALE = 1.0 / math.sqrt(128)
+_BF16 = torch.bfloat16
 
 
 def _pad4(n):
@@ -104,8 +105,11 @@ class PagedCache:
         self.tokens = tokens.view(self.token_cap, 4)
         self.tokens.fill_(-1)
         self._index = streams.get_device()
+        self._table_bytes = wan.rope3d_table_bytes(grid)
+        if self._table_bytes == 0:
+            raise ValueError("grid %r has no RoPE table" % (grid,))
         self._desc = None
-        self._workspace = self._workspace_for = None
+        self._workspace = self._need_for = None
         self._q_shape = torch.Size((self.token_cap, self.heads, 128))
         self._kv_shape = torch.Size((self.token_cap, self.kv_heads, 128))
         self._pool_shape = torch.Size((self.n_pages, self.kv_heads,
@@ -144,19 +148,31 @@ class PagedCache:
         d.max_new = self.max_new
         return d
 
-    def _check(self, shape, *named):
-        """Contiguous bf16 tensors of one shape on the cache's device."""
-        for name, t in named:
-            if t.dtype != torch.bfloat16 or not t.is_contiguous():
-                raise ValueError("%s must be a contiguous bf16 tensor" % name)
-            if t.shape != shape:
-                wan._shape_is(t, shape, name)
-        self._here(*named)
+    def _check(self, shape, name, t):
+        """t is a contiguous bf16 tensor of the shape, on the cache's
+        device."""
+        if t.dtype != _BF16 or not t.is_contiguous():
+            raise ValueError("%s must be a contiguous bf16 tensor" % name)
+        if t.shape != shape:
+            wan._shape_is(t, shape, name)
+        if t.get_device() != self._index:
+            wan._on_cuda(("streams", self.streams), (name, t))
 
-    def _here(self, *named):
-        for name, t in named:
-            if t.get_device() != self._index:
-                wan._on_cuda(("streams", self.streams), (name, t))
+    def _weights(self, n, name, t):
+        if t.dtype != torch.float32 or not t.is_contiguous() \
+                or t.numel() != n:
+            wan._f32_n(t, n, name)
+        if t.get_device() != self._index:
+            wan._on_cuda(("streams", self.streams), (name, t))
+
+    def _bytes(self, need, name, t):
+        if not t.is_contiguous():
+            raise ValueError("%s must be a contiguous tensor" % name)
+        if t.numel() * t.element_size() < need:
+            raise ValueError("%s holds %d bytes, %d are needed"
+                             % (name, t.numel() * t.element_size(), need))
+        if t.get_device() != self._index:
+            wan._on_cuda(("streams", self.streams), (name, t))
 
     def plan(self, new_lens, stream=None):
         """Plans a step: new_lens int32 CUDA tensor [R], > 0 new tokens of
@@ -164,7 +180,8 @@ class PagedCache:
         if new_lens.dtype != torch.int32 or not new_lens.is_contiguous():
             raise ValueError("new_lens must be a contiguous int32 tensor")
         wan._shape_is(new_lens, (self.n_streams,), "new_lens")
-        self._here(("new_lens", new_lens))
+        if new_lens.get_device() != self._index:
+            wan._on_cuda(("streams", self.streams), ("new_lens", new_lens))
         wan.paged_plan(self.descriptor(), new_lens, stream=stream)
 
     def write(self, q, k, v, wq, wk, table, k_pages, v_pages, q_out=None,
@@ -172,44 +189,52 @@ class PagedCache:
         """QK-Norm and RoPE of the planned rows: q into q_out (default: in
         place), k into its slots of k_pages; v into v_pages
         (wan_paged_write)."""
-        q_out = q if q_out is None else q_out
-        self._check(self._q_shape, ("q", q), ("q_out", q_out))
-        self._check(self._kv_shape, ("k", k), ("v", v))
-        self._check(self._pool_shape, ("k_pages", k_pages),
-                    ("v_pages", v_pages))
-        wan._f32_n(wq, self.heads * 128, "wq")
-        wan._f32_n(wk, self.kv_heads * 128, "wk")
+        self._check(self._q_shape, "q", q)
+        if q_out is None:
+            q_out = q
+        else:
+            self._check(self._q_shape, "q_out", q_out)
+        self._check(self._kv_shape, "k", k)
+        self._check(self._kv_shape, "v", v)
+        self._check(self._pool_shape, "k_pages", k_pages)
+        self._check(self._pool_shape, "v_pages", v_pages)
+        self._weights(self.heads * 128, "wq", wq)
+        self._weights(self.kv_heads * 128, "wk", wk)
         if table is None:
             raise ValueError("write needs a RoPE table")
-        wan._check_table(table, self.grid, 128)
-        self._here(("wq", wq), ("wk", wk), ("table", table))
+        self._bytes(self._table_bytes, "table", table)
         wan.paged_write(self.descriptor(), q, q_out, k, v, wq, wk, k_pages,
                         v_pages, table, eps, stream=stream)
 
+    def workspace_bytes(self):
+        """Scratch an attention call needs."""
+        if self._need_for != self.max_new:
+            self._need = wan.paged_workspace_bytes(self.descriptor(),
+                                                   self.device)
+            self._need_for = self.max_new
+        return self._need
+
     def workspace(self):
-        """The attention's scratch of this cache, allocated on first use.
-        Calls that overlap on the device need one each (``attn``'s
-        workspace argument)."""
-        if self._workspace is None or self._workspace_for != self.max_new:
-            need = wan.paged_workspace_bytes(self.descriptor(), self.device)
-            if self._workspace is None or self._workspace.numel() < need:
-                self._workspace = torch.empty(need, dtype=torch.uint8,
-                                              device=self.device)
-            self._workspace_for = self.max_new
+        """The cache's own scratch, allocated on first use.  Calls that
+        overlap on the device need one each (``attn``'s workspace
+        argument)."""
+        need = self.workspace_bytes()
+        if self._workspace is None or self._workspace.numel() < need:
+            self._workspace = torch.empty(need, dtype=torch.uint8,
+                                          device=self.device)
         return self._workspace
 
     def attn(self, q, k_pages, v_pages, o, softmax_scale=_SCALE, stream=None,
              workspace=None):
         """o = softmax(q K^T scale) V over the pages for the planned rows
         (wan_paged_attn)."""
-        self._check(self._q_shape, ("q", q), ("o", o))
-        self._check(self._pool_shape, ("k_pages", k_pages),
-                    ("v_pages", v_pages))
+        self._check(self._q_shape, "q", q)
+        self._check(self._q_shape, "o", o)
+        self._check(self._pool_shape, "k_pages", k_pages)
+        self._check(self._pool_shape, "v_pages", v_pages)
         if workspace is None:
             workspace = self.workspace()
         else:
-            self._here(("workspace", workspace))
-            if not workspace.is_contiguous():
-                raise ValueError("workspace must be a contiguous tensor")
+            self._bytes(self.workspace_bytes(), "workspace", workspace)
         wan.paged_attn(self.descriptor(), q, k_pages, v_pages, o,
                        softmax_scale, workspace, stream=stream)

@@ -623,8 +623,13 @@ def _paged_call(name, t, stream, *args):
         with torch.cuda.device(index):
             return _paged_call(name, t, stream, *args)
     if stream is None:
-        stream = torch.cuda.current_stream()
-    _check(getattr(lib(), name)(*args, stream.cuda_stream), name)
+        # the handle alone: building a Stream object takes 3 us a call
+        raw = torch._C._cuda_getCurrentRawStream(index)
+    else:
+        raw = stream.cuda_stream
+    st = getattr(_lib or lib(), name)(*args, raw)
+    if st:
+        _check(st, name)
 
 
 def paged_plan(desc, new_lens, stream=None):
