@@ -90,7 +90,10 @@ __device__ __forceinline__ void cluster_wait() {
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-__device__ __forceinline__ uint64_t block_scan(uint64_t v, uint64_t* red) {
+// Inclusive sum over the block's threads.  one_warp: only the first 32
+// threads have values (up to 32 streams): one level of the two.
+__device__ __forceinline__ uint64_t block_scan(uint64_t v, uint64_t* red,
+                                               bool one_warp = false) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -100,6 +103,7 @@ __device__ __forceinline__ uint64_t block_scan(uint64_t v, uint64_t* red) {
   __syncthreads();  // red is reused by consecutive calls
   if (lane == 31) red[warp] = v;
   __syncthreads();
+  if (one_warp) return warp ? red[0] : v;
   if (warp == 0) {
     uint64_t t = red[lane];
 #pragma unroll
@@ -143,7 +147,8 @@ __device__ void build_few(const PlanArgs& a, int ql, int kv, int q0, int lo,
   const int stage0 = on ? min(lo, kv - 1) / kStage : 0;
   const int n = on ? (kv + kStage - 1) / kStage - stage0 : 0;
   const uint64_t sc = block_scan(
-      (static_cast<uint64_t>(on) << 40) | static_cast<uint64_t>(n), red);
+      (static_cast<uint64_t>(on) << 40) | static_cast<uint64_t>(n), red,
+      a.c.n_streams <= 32);
   const int idx = static_cast<int>(sc >> 40) - on;
   const int base = static_cast<int>(sc & 0xFFFFFFFFFFull) - n;
   if (on) {
@@ -218,6 +223,7 @@ __device__ void build_tiles(const PlanArgs& a, int ql, int nb, uint64_t* red,
                             const WorkMem& mem) {
   const int r = threadIdx.x;
   const bool on = ql > 0;
+  const bool small = a.c.n_streams <= 32;
   const int heads = a.c.heads;
   __shared__ int s_units, s_act;
   __shared__ unsigned long long s_top, s_sum;
@@ -240,12 +246,12 @@ __device__ void build_tiles(const PlanArgs& a, int ql, int nb, uint64_t* red,
   const int m_full = full_weight(w_nb), m_last = last_weight(w_nb, m_ql);
   const int units = m_tiles * heads;
   const int upto =
-      static_cast<int>(block_scan(static_cast<uint64_t>(units), red));
+      static_cast<int>(block_scan(static_cast<uint64_t>(units), red, small));
   const uint64_t weight =
       mine ? static_cast<uint64_t>(heads) *
                  (static_cast<uint64_t>(m_tiles - 1) * m_full + m_last)
            : 0;
-  const uint64_t all = block_scan(weight, red);
+  const uint64_t all = block_scan(weight, red, small);
   __syncthreads();
   mem.a[r] = upto;           // units up to and with the r-th stream
   mem.b[r] = m_tiles;
@@ -264,32 +270,37 @@ __device__ void build_tiles(const PlanArgs& a, int ql, int nb, uint64_t* red,
   if (U < G) G = static_cast<int>(min(static_cast<int64_t>(G),
                                       max(static_cast<int64_t>(U), parts)));
   if (G < 1) G = 1;
-  // Loads of the CTAs after K rounds; the most rounds whose heaviest CTA
-  // stays within the mean (at most two fewer than there are: the rounds go
-  // up and down, which leaves little beyond the last unit's length).
-  const int share = kPlanThreads / G;  // threads of one CTA's sum
+  // Loads of the CTAs after K rounds, `share` threads a CTA; the most rounds
+  // whose heaviest CTA stays within the mean, at most two fewer than there
+  // are (the rounds go up and down, which leaves little beyond a unit's
+  // length between the CTAs).
+  const int share = kPlanThreads / G;
   const int c = r % G, part = r / G;
+  auto unit_weight = [&](int u) {
+    const int i = find_stream(mem.a, n_act, u);
+    const int at = u - (i ? mem.a[i - 1] : 0);
+    return at % mem.b[i] == 0 ? mem.d[i] : mem.c[i];
+  };
   int K = U / G;
+  if (r < G) s_load[r] = 0;
+  if (r == 0) s_top = 0;
+  __syncthreads();
+  if (part < share && part < K) {
+    unsigned long long sum = 0;
+    for (int k = part; k < K; k += share)
+      sum += unit_weight(k * G + (k & 1 ? G - 1 - c : c));
+    atomicAdd(&s_load[c], sum);
+  }
   for (int tries = 0;; ++tries) {
-    if (r < G) s_load[r] = 0;
-    if (r == 0) s_top = 0;
-    __syncthreads();
-    if (part < share) {
-      unsigned long long sum = 0;
-      for (int k = part; k < K; k += share) {
-        const int u = k * G + (k & 1 ? G - 1 - c : c);
-        const int i = find_stream(mem.a, n_act, u);
-        const int at = u - (i ? mem.a[i - 1] : 0);
-        sum += at % mem.b[i] == 0 ? mem.d[i] : mem.c[i];
-      }
-      atomicAdd(&s_load[c], sum);
-    }
     __syncthreads();
     if (r < G) atomicMax(&s_top, s_load[r]);
     __syncthreads();
     if (K == 0 || tries == 2 || s_top * G <= s_sum) break;
     --K;
     __syncthreads();
+    if (r < G)
+      s_load[r] -= unit_weight(K * G + (K & 1 ? G - 1 - r : r));
+    if (r == 0) s_top = 0;
   }
   // the line: places in proportion to what each CTA lacks
   const uint64_t mean = (s_sum + G - 1) / G;
@@ -305,7 +316,7 @@ __device__ void build_tiles(const PlanArgs& a, int ql, int nb, uint64_t* red,
   const uint64_t skipped = static_cast<uint64_t>(before - rag) * m_full +
                            static_cast<uint64_t>(rag) * m_last;
   const uint64_t on_line = weight - (mine ? skipped : 0);
-  const uint64_t line_upto = block_scan(on_line, red);
+  const uint64_t line_upto = block_scan(on_line, red, small);
   __shared__ unsigned long long s_lack, s_line;
   if (r == kPlanThreads - 1) {
     s_lack = lack_upto;
@@ -391,7 +402,7 @@ __global__ void __launch_bounds__(kPlanThreads)
   const int rows = max(nw, 0);
   const bool ended = nw < 0;
   const int64_t end =
-      static_cast<int64_t>(block_scan(static_cast<uint64_t>(rows), red));
+      static_cast<int64_t>(block_scan(static_cast<uint64_t>(rows), red, R <= 32));
   const int64_t total = static_cast<int64_t>(old) + rows;
   const int64_t cap = c.token_cap;
   const bool fit =
@@ -415,7 +426,8 @@ __global__ void __launch_bounds__(kPlanThreads)
       valid ? static_cast<int>((total + ps - 1) >> a.page_shift) : held;
   const int need = valid ? top - held : 0;
   const uint64_t sums = block_scan(
-      (static_cast<uint64_t>(back) << 32) | static_cast<uint64_t>(need), red);
+      (static_cast<uint64_t>(back) << 32) | static_cast<uint64_t>(need), red,
+      R <= 32);
   const int back_incl = static_cast<int>(sums >> 32);
   const int need_incl = static_cast<int>(sums & 0xFFFFFFFFull);
   s_back[r] = back_incl;
@@ -437,7 +449,7 @@ __global__ void __launch_bounds__(kPlanThreads)
   // admission stops for good at the first stream that does not fit, so the
   // admitted needs are a prefix of the line of needs
   const int n_out = static_cast<int>(
-      block_scan(admit ? static_cast<uint64_t>(need) : 0ull, red));
+      block_scan(admit ? static_cast<uint64_t>(need) : 0ull, red, R <= 32));
   __shared__ int s_out;
   if (r == kPlanThreads - 1) s_out = n_out;
   const int kv = ended ? 0 : old + (admit ? rows : 0);

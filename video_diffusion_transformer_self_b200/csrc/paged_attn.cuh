@@ -590,7 +590,9 @@ __global__ void __launch_bounds__(128)
 // persistent CTA per SM walks its share of the plan's division: rounds of
 // whole units (256 rows of a stream, head), then its part of the line of the
 // last units, so that all CTAs end together whatever the streams' lengths.
-// A unit whose rows fit one tile runs that tile alone.
+// A unit whose rows fit one tile gives both tiles the same Q rows and every
+// other key block: the two softmax chains still hide each other (one chain
+// alone takes about 1 us a block), and the halves are joined at the end.
 // Output rows are staged in the tile's own Q buffer (free once the unit's
 // last P V is done) and stored 512 contiguous bytes a warp instruction with
 // a row check, since a stream's last tile ends inside the next stream's rows
@@ -607,7 +609,8 @@ enum : int {
   PREADY = SFULL + QT,     // per tile: 4 warps stored P
   OFINAL = PREADY + QT,    // per tile: a unit's last P V done
   TFREE = OFINAL + QT,     // per tile: O read and Q buffer free (4 warps)
-  DRAIN = TFREE + QT,
+  HALF1 = TFREE + QT,      // tile 1's half of a shared unit is done (4 warps)
+  DRAIN = HALF1 + 1,
   NBAR
 };
 
@@ -748,6 +751,7 @@ __global__ void __launch_bounds__(wan::kThreads, 1)
   __shared__ __align__(8) uint64_t bar[NBAR];
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
+  __shared__ float2 s_half[BM];  // tile 1's (row max, row sum), shared units
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   if (__ldg(args.c.work + pg::H_MODE) != pg::kModeTile ||
@@ -779,6 +783,7 @@ __global__ void __launch_bounds__(wan::kThreads, 1)
       mbar_init(&bar[OFINAL + t], 1);
       mbar_init(&bar[TFREE + t], 4);
     }
+    mbar_init(&bar[HALF1], 4);
     mbar_init(&bar[DRAIN], 1);
     fence_mbar_init();
   }
@@ -803,7 +808,7 @@ __global__ void __launch_bounds__(wan::kThreads, 1)
       const int in_mask = (1 << args.page_shift) - 1;
       const int row0 = lane << args.box_shift;  // this lane's box
       bool ok = true;
-      int nq = 0, nq1 = 0, nk = 0, nv = 0;  // units, with a 2nd tile; blocks
+      int nq = 0, nq1 = 0, nk = 0, nv = 0;  // units of tile 0, of tile 1; blocks
       Unit c;
       for (Walk w = walk_begin(args); ok && unit_at(args, w, c);) {
         walk_next(args, w, c.span);
@@ -826,7 +831,7 @@ __global__ void __launch_bounds__(wan::kThreads, 1)
           }
         }
         ++nq;
-        nq1 += two;
+        nq1 += two || c.nblk > 1;
         const int kvhead = c.head / args.group;
         for (int j = 0; j < c.nblk && ok; ++j) {
           const int g = nk;
@@ -876,8 +881,9 @@ __global__ void __launch_bounds__(wan::kThreads, 1)
       const uint64_t dk = sdesc_sw128(smem_u32(sK), 16, 1024);
       const uint64_t dv = sdesc_sw128(smem_u32(sV), HALF, 1024);
       const bool leader = elect_one();
-      auto issue_s = [&](int t, int g) {
-        const uint64_t a0 = dq + ((t * TILE) >> 4);
+      // scores of tile t (whose Q rows are in buffer qb) for ring block g
+      auto issue_s = [&](int t, int qb, int g) {
+        const uint64_t a0 = dq + ((qb * TILE) >> 4);
         const uint64_t b0 = dk + (((g % NSK) * TILE) >> 4);
         const uint32_t d = tmem + t * 128;
         if (leader) {
@@ -937,54 +943,84 @@ __global__ void __launch_bounds__(wan::kThreads, 1)
         return true;
       };
       bool ok = true;
-      int g0 = 0, h0 = 0;  // blocks of earlier units: all, with a 2nd tile
-      int n0 = 0, n1 = 0;  // units before this one, with a 2nd tile
+      int g0 = 0;              // ring blocks of earlier units
+      int b0 = 0, b1 = 0;      // blocks of each tile in earlier units
+      int n0 = 0, n1 = 0;      // units of each tile before this one
       Unit c;
       for (Walk w = walk_begin(args); ok && unit_at(args, w, c);) {
         walk_next(args, w, c.span);
         if (c.nblk == 0) continue;
         const bool two = c.rows > BM;
         ok = wait_warp(&bar[QFULL], n0 & 1, abort_flag, status);
-        for (int j = 0; j < c.nblk && ok; ++j) {
-          const int g = g0 + j;
-          if (j > 0) {
-            ok = ready_v(g - 1, c.kb0 + j - 1, c) &&
-                 pv(0, g - 1, g - 1, j - 1, n0);
-            if (!ok) break;
-          }
-          ok = wait_warp(&bar[KFULL + g % NSK], (g / NSK) & 1, abort_flag,
-                         status);
-          if (!ok) break;
-          tc_fence_after();
-          issue_s(0, g);
-          if (j > 0) {
-            if (two) {
-              ok = pv(1, g - 1, h0 + j - 1, j - 1, n1);
+        if (two) {
+          for (int j = 0; j < c.nblk && ok; ++j) {
+            const int g = g0 + j;
+            if (j > 0) {
+              ok = ready_v(g - 1, c.kb0 + j - 1, c) &&
+                   pv(0, g - 1, b0 + j - 1, j - 1, n0);
               if (!ok) break;
             }
-            commit(&bar[VEMPTY + (g - 1) % NSV]);
+            ok = wait_warp(&bar[KFULL + g % NSK], (g / NSK) & 1, abort_flag,
+                           status);
+            if (!ok) break;
+            tc_fence_after();
+            issue_s(0, 0, g);
+            if (j > 0) {
+              ok = pv(1, g - 1, b1 + j - 1, j - 1, n1);
+              if (!ok) break;
+              commit(&bar[VEMPTY + (g - 1) % NSV]);
+            }
+            issue_s(1, 1, g);
+            commit(&bar[KEMPTY + g % NSK]);
           }
-          if (two) issue_s(1, g);
-          commit(&bar[KEMPTY + g % NSK]);
-        }
-        if (ok) {
-          const int jl = c.nblk - 1, g = g0 + jl;
-          ok = ready_v(g, c.kb0 + jl, c) && pv(0, g, g, jl, n0);
           if (ok) {
-            commit(&bar[OFINAL + 0]);
-            if (two) {
-              ok = pv(1, g, h0 + jl, jl, n1);
-              if (ok) commit(&bar[OFINAL + 1]);
+            const int jl = c.nblk - 1, g = g0 + jl;
+            ok = ready_v(g, c.kb0 + jl, c) && pv(0, g, b0 + jl, jl, n0);
+            if (ok) {
+              commit(&bar[OFINAL + 0]);
+              ok = pv(1, g, b1 + jl, jl, n1);
+            }
+            if (ok) {
+              commit(&bar[OFINAL + 1]);
+              commit(&bar[VEMPTY + g % NSV]);
             }
           }
-          if (ok) commit(&bar[VEMPTY + g % NSV]);
+          b0 += c.nblk;
+          b1 += c.nblk;
+          ++n0;
+          ++n1;
+        } else {
+          // one row tile: block j runs on tile j & 1, its P V two blocks on
+          const int pairs = c.nblk > 1 ? 2 : 1;
+          for (int j = 0; j < c.nblk + pairs && ok; ++j) {
+            const int t = pairs == 2 ? j & 1 : 0;
+            if (j >= pairs) {
+              const int jv = j - pairs, g = g0 + jv, own = jv / pairs;
+              ok = ready_v(g, c.kb0 + jv, c) &&
+                   pv(t, g, (t ? b1 : b0) + own, own, t ? n1 : n0);
+              if (!ok) break;
+              commit(&bar[VEMPTY + g % NSV]);
+              // the tile's last block
+              if (j >= c.nblk) commit(&bar[OFINAL + t]);
+            }
+            if (j < c.nblk) {
+              const int g = g0 + j;
+              ok = wait_warp(&bar[KFULL + g % NSK], (g / NSK) & 1, abort_flag,
+                             status);
+              if (!ok) break;
+              tc_fence_after();
+              issue_s(t, 0, g);
+              commit(&bar[KEMPTY + g % NSK]);
+            }
+          }
+          b0 += (c.nblk + pairs - 1) / pairs;
+          ++n0;
+          if (pairs == 2) {
+            b1 += c.nblk / 2;
+            ++n1;
+          }
         }
         g0 += c.nblk;
-        ++n0;
-        if (two) {
-          h0 += c.nblk;
-          ++n1;
-        }
       }
       commit(&bar[DRAIN]);
       wait_warp_drain(&bar[DRAIN], 0, status);
@@ -1000,23 +1036,32 @@ __global__ void __launch_bounds__(wan::kThreads, 1)
     const uint32_t o_col = lane_base + TM_O + t * 128;
     const float c2 = args.scale_log2;
     bool ok = true;
-    uint32_t sph = 0, uph = 0;  // phases of this tile's scores and units
+    // phases of this tile's scores, its units and its shared units
+    uint32_t sph = 0, uph = 0, hph = 0;
     for (Walk w = walk_begin(args); ok;) {
-      int nblk, span, lim_lo = 0, lim_hi = INT32_MAX;
+      int nblk, lim_lo = 0, lim_hi = INT32_MAX;
+      int key_step = BN;  // keys from one of this tile's blocks to the next
       {
         Unit c;
         if (!unit_at(args, w, c)) break;
-        span = c.span;
         nblk = c.nblk;
+        int row = t * BM + r;
+        if (c.rows <= BM) {
+          if (nblk > 1) {  // shared: every other block, the same rows
+            row = r;
+            nblk = (nblk + 1 - t) >> 1;
+            key_step = 2 * BN;
+            c.kb0 += t;
+          } else if (t > 0) {
+            walk_next(args, w, c.span);
+            continue;
+          }
+        }
         // rows behind the tile's last take part unmasked, never written
-        if (t * BM + r < c.rows) {
-          const int a = c.a0 + t * BM + r;
+        if (row < c.rows) {
+          const int a = c.a0 + row;
           lim_lo = pg::key_lo(max(a, 0), c.chunk, c.window) - c.kb0 * BN;
           lim_hi = pg::key_hi(a, c.chunk, c.kv) - c.kb0 * BN;
-        }
-        if (t * BM >= c.rows) {  // a unit of one tile
-          walk_next(args, w, span);
-          continue;
         }
       }
       float m_run = -INFINITY;
@@ -1036,8 +1081,8 @@ __global__ void __launch_bounds__(wan::kThreads, 1)
           for (int c = 0; c < BN; ++c)
             if (c >= lim_hi || c < lim_lo) s[c] = -INFINITY;
         }
-        lim_lo -= BN;
-        lim_hi -= BN;
+        lim_lo -= key_step;
+        lim_hi -= key_step;
         const float mx = (masked ? rowmax_masked<BN>(s) : rowmax<BN>(s)) * c2;
         if (j == 0) {
           m_run = mx;
@@ -1093,6 +1138,39 @@ __global__ void __launch_bounds__(wan::kThreads, 1)
       Unit ce;
       unit_at(args, w, ce);
       walk_next(args, w, ce.span);
+      const bool shared = ce.rows <= BM && ce.nblk > 1;
+      float f0 = 1.f, f1 = 0.f;  // factors of the halves of a shared unit
+      if (shared) {
+        if (t == 1) {
+          s_half[r] = make_float2(m_run, l_run);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar[HALF1]);
+          continue;  // tile 0's warps read O of both and free both
+        }
+        ok = wait_warp(&bar[HALF1], hph, abort_flag, status);
+        if (!ok) break;
+        hph ^= 1;
+        tc_fence_after();
+        const float2 other = s_half[r];
+        const float mn = fmaxf(m_run, other.x);
+        f0 = m_run == -INFINITY ? 0.f : ex2(m_run - mn);
+        f1 = other.x == -INFINITY ? 0.f : ex2(other.x - mn);
+        l_run = l_run * f0 + other.y * f1;
+        m_run = mn;
+      }
+      // 32 columns of O, the halves joined
+      auto load_o = [&](int col, float (&o)[32]) {
+        tmem_ld32(o_col + col, o);
+        tmem_ld_wait32(o);
+        if (shared) {
+          float o1[32];
+          tmem_ld32(o_col + 128 + col, o1);
+          tmem_ld_wait32(o1);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = o[e] * f0 + o1[e] * f1;
+        }
+      };
       const int wrow0 = (warp & 3) * 32;  // this warp's rows of the tile
       const int live = min(ce.rows - t * BM - wrow0,
                            args.c.token_cap - ce.q0 - t * BM - wrow0);
@@ -1129,8 +1207,7 @@ __global__ void __launch_bounds__(wan::kThreads, 1)
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
               float o[32];
-              tmem_ld32(o_col + hc * 64 + c * 32, o);
-              tmem_ld_wait32(o);
+              load_o(hc * 64 + c * 32, o);
 #pragma unroll
               for (int e = 0; e < 8; ++e)
                 stage(c * 8 + e,
@@ -1161,8 +1238,7 @@ __global__ void __launch_bounds__(wan::kThreads, 1)
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           float o[32];
-          tmem_ld32(o_col + c * 32, o);
-          tmem_ld_wait32(o);
+          load_o(c * 32, o);
 #pragma unroll
           for (int e = 0; e < 4; ++e)
             stage(c * 4 + e,
@@ -1180,7 +1256,10 @@ __global__ void __launch_bounds__(wan::kThreads, 1)
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bar[TFREE + t]);
+        if (lane == 0) {
+          mbar_arrive(&bar[TFREE + t]);
+          if (shared) mbar_arrive(&bar[TFREE + 1]);
+        }
       }
     }
   }
