@@ -132,8 +132,10 @@ __device__ __forceinline__ int find_stream(const int* incl, int n, int x) {
 
 // Scratch of build_work, one entry a stream or CTA.
 struct WorkMem {
-  int *a, *b, *c, *d;
-  unsigned long long* load;
+  int *a, *b, *c, *d, *e, *f;
+  const int* end;             // packed rows up to and with each stream
+  unsigned long long* load;   // one a CTA
+  int64_t* start;             // one a stream
 };
 
 // The few-row kernel's line: 64-key stages from the first row's first key to
@@ -309,13 +311,11 @@ __device__ void build_tiles(const PlanArgs& a, int ql, int nb, uint64_t* red,
   const uint64_t lack_upto = block_scan(lack, red);
   const int first = K * G;  // units before the line
   const int base = upto - units;
-  // ragged pairs (every m_tiles-th unit, the first of a head) among the
-  // stream's units before the line
+  // the stream's units before the line
   const int before = min(max(first - base, 0), units);
-  const int rag = mine ? (before + m_tiles - 1) / m_tiles : 0;
-  const uint64_t skipped = static_cast<uint64_t>(before - rag) * m_full +
-                           static_cast<uint64_t>(rag) * m_last;
-  const uint64_t on_line = weight - (mine ? skipped : 0);
+  const uint64_t skipped =
+      mine ? weight_before(before, m_tiles, m_full, m_last) : 0;
+  const uint64_t on_line = weight - skipped;
   const uint64_t line_upto = block_scan(on_line, red, small);
   __shared__ unsigned long long s_lack, s_line;
   if (r == kPlanThreads - 1) {
@@ -324,12 +324,16 @@ __device__ void build_tiles(const PlanArgs& a, int ql, int nb, uint64_t* red,
   }
   __syncthreads();
   int32_t* work = a.c.work;
+  // (the line and the lacks are below 2^30: three rounds of weights)
+  int* s_cut = reinterpret_cast<int*>(s_load);
+  __syncthreads();
   if (r < G) {
-    // (the line and the lacks are below 2^30: three rounds of weights)
-    work[kLine + r + 1] =
+    const int end =
         r == G - 1 ? static_cast<int>(s_line)
                    : static_cast<int>(s_lack ? s_line * lack_upto / s_lack : 0);
-    if (r == 0) work[kLine] = 0;
+    s_cut[r + 1] = end;
+    work[kLine + r + 1] = end;
+    if (r == 0) s_cut[0] = work[kLine] = 0;
   }
   if (mine) {
     int32_t* e = work + kHdr + kEnt * r;
@@ -338,9 +342,38 @@ __device__ void build_tiles(const PlanArgs& a, int ql, int nb, uint64_t* red,
     e[E_COUNT] = m_tiles;
     e[E_FULL] = m_full;
     e[E_LAST] = m_last;
-    *reinterpret_cast<int64_t*>(e + E_LINE) =
-        static_cast<int64_t>(line_upto - on_line) -
-        static_cast<int64_t>(skipped);
+    const int64_t start = static_cast<int64_t>(line_upto - on_line) -
+                          static_cast<int64_t>(skipped);
+    *reinterpret_cast<int64_t*>(e + E_LINE) = start;
+    mem.e[r] = src;
+    mem.f[r] = m_ql;
+    mem.start[r] = start;
+  }
+  __syncthreads();
+  // what the joining pass needs of every unit on the line
+  for (int j = r; j < U - first; j += kPlanThreads) {
+    const int u = first + j;
+    const int i = find_stream(mem.a, n_act, u);
+    const int local = u - (i ? mem.a[i - 1] : 0);
+    const int tiles = mem.b[i];
+    const int head = local / tiles, tile = local - head * tiles;
+    const int x0 = static_cast<int>(
+        mem.start[i] + weight_before(local, tiles, mem.c[i], mem.d[i]));
+    const int x1 = x0 + (tile == 0 ? mem.d[i] : mem.c[i]) - 1;
+    // CTAs that hold its first and its last place
+    const int c0 = find_stream(s_cut + 1, G, x0);
+    const int c1 = find_stream(s_cut + 1, G, x1);
+    const int row0 = (tiles - 1 - tile) * kTileRows;
+    int32_t rec[kJoinInts] = {0, 0, 0, 0, 0, 0, 0, 0};
+    rec[J_ROW] = (mem.e[i] ? mem.end[mem.e[i] - 1] : 0) + row0;
+    rec[J_ROWS] = c0 == c1 ? 0 : min(mem.f[i] - row0, kTileRows);
+    rec[J_HEAD] = head;
+    rec[J_PART] = 2 * c0 + (x0 > s_cut[c0] ? 1 : 0);
+    rec[J_CTA] = c0 + 1;
+    rec[J_PARTS] = c1 - c0 + 1;
+    int4* dst = reinterpret_cast<int4*>(work + kJoin + kJoinInts * j);
+    dst[0] = make_int4(rec[0], rec[1], rec[2], rec[3]);
+    dst[1] = make_int4(rec[4], rec[5], rec[6], rec[7]);
   }
   if (r == 0) {
     work[H_MODE] = kModeTile;
@@ -382,7 +415,7 @@ __global__ void __launch_bounds__(kPlanThreads)
   int* s_hw = s_dims;
   int* s_w = s_dims + kMaxStreams;
   __shared__ uint32_t s_mhw[kMaxStreams];
-  __shared__ uint32_t s_mw[kMaxStreams];
+  __shared__ __align__(8) uint32_t s_mw[kMaxStreams];
   const wan_paged_t& c = a.c;
   const int R = c.n_streams;
   const int r = threadIdx.x;
@@ -452,6 +485,15 @@ __global__ void __launch_bounds__(kPlanThreads)
       block_scan(admit ? static_cast<uint64_t>(need) : 0ull, red, R <= 32));
   __shared__ int s_out;
   if (r == kPlanThreads - 1) s_out = n_out;
+  const WorkMem mem = {s_back,
+                       s_need,
+                       s_from,
+                       s_rows,
+                       s_old,
+                       reinterpret_cast<int*>(s_mhw),
+                       s_end,
+                       reinterpret_cast<unsigned long long*>(s_mw),
+                       reinterpret_cast<int64_t*>(s_dims)};
   const int kv = ended ? 0 : old + (admit ? rows : 0);
   const int ctas = gridDim.x;
   const int rank = blockIdx.x;
@@ -474,8 +516,7 @@ __global__ void __launch_bounds__(kPlanThreads)
   if (ctas > 1) cluster_arrive();
   if (rank == movers) {
     build_work(a, admit ? rows : 0, kv, r ? s_end[r - 1] : 0, cfg.z, cfg.w,
-               red, WorkMem{s_back, s_need, s_from, s_rows,
-                            reinterpret_cast<unsigned long long*>(s_dims)});
+               red, mem);
     __syncthreads();
     cluster_wait();
     return;
@@ -546,8 +587,7 @@ __global__ void __launch_bounds__(kPlanThreads)
   if (ctas == 1) {
     __syncthreads();
     build_work(a, admit ? rows : 0, kv, r ? s_end[r - 1] : 0, cfg.z, cfg.w,
-               red, WorkMem{s_back, s_need, s_from, s_rows,
-                            reinterpret_cast<unsigned long long*>(s_dims)});
+               red, mem);
   }
 }
 

@@ -28,7 +28,7 @@ constexpr int kStage = 64;
 constexpr int kBlock = 128;
 constexpr int kTileRows = 256;
 constexpr int kFewCtasPerSm = 2;
-constexpr int kMaxCtas = 1023;
+constexpr int kMaxCtas = 511;
 
 // Weight of a unit: 8 a 128-key block with two row tiles, 5 with one, and
 // kUnitWeight for its start and end (measured: see build_tiles).
@@ -36,10 +36,21 @@ constexpr int kPairWeight = 8;
 constexpr int kOneWeight = 5;
 constexpr int kUnitWeight = 24;
 
-// work: a header, LINE[0 .. kMaxCtas], then kEnt ints per active stream.
+// work: a header, LINE[0 .. kMaxCtas], kJoinInts ints per unit of the line
+// (at most three rounds of them), then kEnt ints per active stream.
 constexpr int kLine = 16;
-constexpr int kHdr = kLine + kMaxCtas + 1;
+constexpr int kJoin = kLine + kMaxCtas + 1;
+constexpr int kJoinInts = 8;
+constexpr int kHdr = kJoin + 3 * kMaxCtas * kJoinInts + 8;
 constexpr int kEnt = 8;
+enum : int {
+  J_ROW = 0,    // packed row of the unit's first row
+  J_ROWS = 1,   // its rows, 0: one CTA has the unit to itself
+  J_HEAD = 2,
+  J_PART = 3,   // slot of its first part; the others are 2 c, c from ...
+  J_CTA = 4,    // ... this CTA on
+  J_PARTS = 5   // parts, the first one included
+};
 enum : int {
   H_MODE = 0,     // kMode*
   H_ACTIVE = 1,   // entries
@@ -62,6 +73,15 @@ enum : int {
   E_LINE = 6      // (64 bits) the line's place at which the stream's units
                   // would start, had all of them been on it
 };
+
+// Weight of a stream's units before its unit n (the last tile pair, which
+// may be lighter, is the first unit of each head).
+__host__ __device__ __forceinline__ int64_t weight_before(int n, int tiles,
+                                                          int full, int last) {
+  const int rag = (n + tiles - 1) / tiles;
+  return static_cast<int64_t>(n - rag) * full +
+         static_cast<int64_t>(rag) * last;
+}
 
 // kFew: CTA c of `ctas` takes places [first(c), first(c + 1)) of the line of
 // `total`; the first total % ctas CTAs take one more.

@@ -77,21 +77,31 @@ __device__ __forceinline__ void launch_dependents() {
 }
 
 // Weighted sum of a row's partial results: lane l holds channels 4 l .. + 3.
+template <int kBatch>
 struct JoinAcc {
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   float m = -INFINITY, l = 0.f;
   // Parts 0 .. n - 1 (those that has(k) says were written), part k at
-  // row_of(k) of the workspace.  32 parts at a time: their maxima and sums come with one load a lane, their O rows with
-  // batches of independent loads (loads under a condition ran one after the
-  // other: 25 parts took 13 us instead of 4).
-  static constexpr int kBatch = 16;
+  // row_of(k) of the workspace.  32 parts at a time: their maxima and sums
+  // come with one load a lane, their O rows with batches of independent
+  // loads, the first of them before the maxima are there (loads under a
+  // condition ran one after the other: 25 parts took 13 us instead of 4).
+  // A part without keys is loaded too, whatever it holds, and dropped.
   template <typename RowOf, typename Has>
   __device__ __forceinline__ void add_all(int n, int lane, const PagedArgs& a,
                                           RowOf row_of, Has has) {
     for (int k0 = 0; k0 < n; k0 += 32) {
+      const int cnt = min(n - k0, 32);
+      float4 v[kBatch];
+      auto load = [&](int b) {
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k)
+          v[k] = reinterpret_cast<const float4*>(
+              a.part_o + row_of(k0 + min(b + k, cnt - 1)) * HD)[lane];
+      };
       float2 ml = make_float2(-INFINITY, 0.f);
-      if (k0 + lane < n && has(k0 + lane)) ml = a.part_ml[row_of(k0 + lane)];
-      // a part that saw no key has no O
+      if (lane < cnt && has(k0 + lane)) ml = a.part_ml[row_of(k0 + lane)];
+      load(0);
       if (!(ml.y > 0.f)) ml = make_float2(-INFINITY, 0.f);
       float top = ml.x;
 #pragma unroll
@@ -108,15 +118,7 @@ struct JoinAcc {
       l = fmaf(l, w0, sum);
       m = mn;
       acc = make_float4(acc.x * w0, acc.y * w0, acc.z * w0, acc.w * w0);
-      const int cnt = min(n - k0, 32);
-      for (int b = 0; b < cnt; b += kBatch) {
-        // all loads of a batch first (a part without keys is loaded too,
-        // whatever it holds, and dropped)
-        float4 v[kBatch];
-#pragma unroll
-        for (int k = 0; k < kBatch; ++k)
-          v[k] = reinterpret_cast<const float4*>(
-              a.part_o + row_of(k0 + min(b + k, cnt - 1)) * HD)[lane];
+      for (int b = 0;;) {
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
           const float wk = __shfl_sync(0xffffffffu, w, (b + k) & 31);
@@ -127,6 +129,9 @@ struct JoinAcc {
             acc.w = fmaf(v[k].w, wk, acc.w);
           }
         }
+        b += kBatch;
+        if (b >= cnt) break;
+        load(b);
       }
     }
   }
@@ -568,7 +573,7 @@ __global__ void __launch_bounds__(128)
     const int q0 = __ldg(e + pg::E_Q0);
     if (r >= __ldg(e + pg::E_ROWS) * args.group || q0 + i >= args.c.token_cap)
       continue;
-    JoinAcc acc;
+    JoinAcc<16> acc;
     // the first CTA's part is its last one unless the item starts it
     const bool mid = xs > line.first(c0);
     acc.add_all(c1 - c0 + 1, lane, args, [&](int k) {
@@ -652,15 +657,6 @@ __device__ __forceinline__ int cut(int nb, int s, int weight) {
   return static_cast<int>(static_cast<int64_t>(nb) * s / weight);
 }
 
-// Weight of a stream's units before its unit `n` (the last tile pair, which
-// may be lighter, is the first unit of each head).
-__device__ __forceinline__ int64_t weight_before(int n, int tiles, int full,
-                                                 int last) {
-  const int rag = (n + tiles - 1) / tiles;
-  return static_cast<int64_t>(n - rag) * full +
-         static_cast<int64_t>(rag) * last;
-}
-
 // The part at w; false at the end of the CTA's share.
 __device__ __forceinline__ bool unit_at(const PagedArgs& a, const Walk& w,
                                         Unit& t) {
@@ -693,7 +689,7 @@ __device__ __forceinline__ bool unit_at(const PagedArgs& a, const Walk& w,
                                    __ldg(m + pg::E_BASE),
                                0),
                            __ldg(m + pg::E_COUNT) * a.c.heads);
-      if (line + weight_before(skip, __ldg(m + pg::E_COUNT),
+      if (line + pg::weight_before(skip, __ldg(m + pg::E_COUNT),
                                __ldg(m + pg::E_FULL),
                                __ldg(m + pg::E_LAST)) <= w.x)
         lo = mid;
@@ -1271,66 +1267,37 @@ __global__ void __launch_bounds__(wan::kThreads, 1)
   }
 }
 
-// One warp per row of the line's units that several CTAs shared.
+// One warp per row of the line's units that several CTAs shared, from the
+// plan's record of the unit.
 __global__ void __launch_bounds__(128)
     paged_tile_join(const __grid_constant__ PagedArgs args) {
   const int32_t* work = args.c.work;
   if (__ldg(work + pg::H_MODE) != pg::kModeTile) return;
-  const int ctas = __ldg(work + pg::H_CTAS);
-  const int first = __ldg(work + pg::H_WAVES) * ctas;
-  const int n = __ldg(work + pg::H_TOTAL) - first;  // units on the line
-  const int32_t* line = work + pg::kLine;
+  const int n = __ldg(work + pg::H_TOTAL) -
+                __ldg(work + pg::H_WAVES) * __ldg(work + pg::H_CTAS);
+  const int4* recs = reinterpret_cast<const int4*>(work + pg::kJoin);
   const int lane = threadIdx.x & 31;
   const int warps = gridDim.x * 4;
-  const int heads = args.c.heads;
   grid_dependency_wait();
   for (int it = blockIdx.x * 4 + (threadIdx.x >> 5);
        it < n * pg::kTileRows; it += warps) {
-    const int u = first + it / pg::kTileRows;
     const int i = it % pg::kTileRows;
-    const int32_t* e = find_entry(work, pg::E_BASE, 1, u);
-    const int tiles = __ldg(e + pg::E_COUNT);
-    const int full = __ldg(e + pg::E_FULL), last = __ldg(e + pg::E_LAST);
-    const int local = u - __ldg(e + pg::E_BASE);
-    const int head = local / tiles;
-    const int tile = local - head * tiles;
-    const int x0 = static_cast<int>(
-        __ldg(reinterpret_cast<const long long*>(e + pg::E_LINE)) +
-        weight_before(local, tiles, full, last));
-    const int x1 = x0 + (tile == 0 ? last : full) - 1;
-    // CTAs that hold its first and its last place
-    auto holder = [&](int x) {
-      int lo = 0, hi = ctas - 1;
-      while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (__ldg(line + mid + 1) > x)
-          hi = mid;
-        else
-          lo = mid + 1;
-      }
-      return lo;
-    };
-    const int c0 = holder(x0), c1 = holder(x1);
-    if (c0 == c1) continue;
-    const int stream = __ldg(e + pg::E_STREAM);
-    const int tx = tiles - 1 - tile;
-    const int row = tx * pg::kTileRows + i;
-    const int64_t at = static_cast<int64_t>(__ldg(args.c.q_start + stream)) +
-                       row;
-    if (row >= __ldg(args.c.q_lens + stream) || at >= args.c.token_cap)
-      continue;
-    // the first CTA's part is its last one unless the unit starts its share
-    const bool mid = x0 > __ldg(line + c0);
-    JoinAcc acc;
+    const int4 r0 = __ldg(recs + 2 * (it / pg::kTileRows));
+    const int4 r1 = __ldg(recs + 2 * (it / pg::kTileRows) + 1);
+    const int row = r0.x + i;
+    if (i >= r0.y || row >= args.c.token_cap) continue;
+    const int32_t* cut = work + pg::kLine + r1.x - 1;
+    JoinAcc<4> acc;
     acc.add_all(
-        c1 - c0 + 1, lane, args,
+        r1.y, lane, args,
         [&](int k) {
-          return (2ll * (c0 + k) + (k == 0 && mid ? 1 : 0)) * pg::kTileRows +
-                 i;
+          const int slot = k ? 2 * (r1.x - 1 + k) : r0.w;
+          return static_cast<int64_t>(slot) * pg::kTileRows + i;
         },
-        // a CTA between them may have no share of the line
-        [&](int k) { return __ldg(line + c0 + k) < __ldg(line + c0 + k + 1); });
-    acc.write(args.o + (at * heads + head) * HD, lane);
+        // a CTA between the first and the last may have no share of the line
+        [&](int k) { return __ldg(cut + k) < __ldg(cut + k + 1); });
+    acc.write(args.o + (static_cast<int64_t>(row) * args.c.heads + r0.z) * HD,
+              lane);
   }
 }
 }  // namespace tile
