@@ -266,3 +266,99 @@ def test_write_and_attention_over_layers_match_the_whole_video():
         mag = np.abs(f64(v)).max()
         assert np.max(np.abs(a - b)) <= 2 * (2 ** -7 + 1e-3) * mag
         assert np.linalg.norm(a - b) <= 1e-2 * np.linalg.norm(b)
+
+
+def test_class_refuses_tensors_that_do_not_fit():
+    c, oc = make([(4, 4, 16, 0)], (20, 4, 4), 12, 16, 20, 4, 2, 16)
+    kp, vp = c.new_pools()
+    q = rows_bf16(16, 4, 1).cuda()
+    k, v = rows_bf16(16, 2, 2).cuda(), rows_bf16(16, 2, 3).cuda()
+    o = torch.empty_like(q)
+    w4, w2 = torch.ones(512, device="cuda"), torch.ones(256, device="cuda")
+    table = wan.rope3d_table(c.grid)
+    lens = torch.ones(1, dtype=torch.int32, device="cuda")
+    with pytest.raises(ValueError, match="plan"):
+        c.attn(q, kp, vp, o)
+    for bad in (lens.long(), lens.cpu(), lens[:0], lens.repeat(2)):
+        with pytest.raises(ValueError):
+            c.plan(bad)
+    c.plan(lens)
+    good = dict(q=q, k=k, v=v, wq=w4, wk=w2, table=table, k_pages=kp,
+                v_pages=vp)
+    for name, t in good.items():
+        bads = [t.cpu(), t[:-1]]
+        if t.dtype != torch.uint8:
+            bads.append(t.double())
+        for bad in bads:
+            with pytest.raises(ValueError):
+                c.write(**dict(good, **{name: bad}))
+    with pytest.raises(ValueError):
+        c.write(**good, q_out=o[:-1])
+    with pytest.raises(ValueError):
+        c.write(**dict(good, table=None))
+    for args in ((q[:-1], kp, vp, o), (q, kp[:-1], vp, o), (q, kp, vp, o[1:]),
+                 (q.float(), kp, vp, o), (q, kp, vp.cpu(), o),
+                 (q.transpose(0, 1), kp, vp, o)):
+        with pytest.raises(ValueError):
+            c.attn(*args)
+    with pytest.raises(ValueError, match="bytes"):
+        c.attn(q, kp, vp, o, workspace=torch.empty(16, dtype=torch.uint8,
+                                                   device="cuda"))
+    with pytest.raises(wan.WanError):
+        c.attn(q, kp, vp, o, softmax_scale=-1.0)
+    with pytest.raises(wan.WanError):
+        c.attn(q, kp, vp, q)
+    c.max_new = 2                      # another kernel than the plan's
+    with pytest.raises(ValueError, match="max_new"):
+        c.attn(q, kp, vp, o)
+
+
+def test_two_calls_at_once_with_a_workspace_each():
+    streams = [(8, 8, 64, 0)] * 2
+    c, oc = make(streams, (60, 8, 8), 160, 32, 60, 2, 2, 1400, 700)
+    step(c, oc, [700, 650])
+    kp, vp = c.new_pools(2)
+    kp.normal_()
+    vp.normal_()
+    q = [rows_bf16(1400, 2, 9 + i).cuda() for i in range(2)]
+    want, o = [], [torch.zeros_like(q[0]) for _ in range(2)]
+    for i in range(2):
+        c.attn(q[i], kp[i], vp[i], o[i])
+        torch.cuda.synchronize()
+        want.append(o[i].clone())
+        o[i].zero_()
+    ws = [torch.empty(c.workspace_bytes(), dtype=torch.uint8, device="cuda")
+          for _ in range(2)]
+    side = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for i in range(2):
+            c.attn(q[i], kp[i], vp[i], o[i], stream=side[i],
+                   workspace=ws[i])
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert torch.equal(o[i], want[i])
+
+
+@pytest.mark.parametrize("seed", range(12))
+def test_random_streams(seed):
+    """Seeded shapes of both kernels: streams, windows, chunks, heads, page
+    sizes, lengths; three steps each, every one checked."""
+    rng = np.random.default_rng(1000 + seed)
+    few = seed % 2 == 0
+    kv_heads = int(rng.integers(1, 4))
+    group = int(rng.integers(1, 5))
+    R = int(rng.integers(1, 7))
+    ps = int(rng.choice([16, 32, 64, 128]))
+    max_new = max(1, int(rng.integers(1, 17)) // group) if few \
+        else int(rng.integers(17, 420))
+    streams = [(4, 5, int(rng.choice([1, 7, 20, 60, 10 ** 9])),
+                int(rng.choice([0, 0, 5, 33, 100, 400]))) for _ in range(R)]
+    steps = []
+    for _ in range(8 if few else 3):
+        new = rng.integers(0, max_new + 1, R)
+        new[rng.random(R) < 0.1] = -1
+        steps.append([int(x) for x in new])
+    _run(streams, (400, 4, 5), ps, kv_heads * group, kv_heads, steps,
+         3000 + seed, max_new, 40 * R + 100,
+         check=(1, len(steps) - 2, len(steps) - 1))

@@ -26,7 +26,7 @@ int check_cache(const wan_paged_t* c) {
     return WAN_EINVAL;
   const int64_t lim = 1ll << 31;
   if (static_cast<int64_t>(c->n_streams) * c->max_pages >= lim ||
-      static_cast<int64_t>(c->max_pages) * c->page_size >= lim ||
+      static_cast<int64_t>(c->max_pages) * c->page_size > lim / 2 ||
       static_cast<int64_t>(c->n_pages) * c->page_size >= lim ||
       static_cast<int64_t>(c->token_cap) * c->heads >= lim ||
       (static_cast<int64_t>(c->n_pages) * c->page_size / kStage +
@@ -59,21 +59,6 @@ namespace {
 // another kernel.
 constexpr int kPlanThreads = 1024;
 
-// Division of 0 <= n < 2^31 by 1 <= d < 2^31 as (n * m) >> (31 + s) with
-// s = ceil(log2 d), m = floor(2^(31 + s) / d) + 1: m exceeds 2^(31 + s) / d
-// by at most 1, which adds less than n 2^-(31 + s) < 2^-s <= 1 / d to the
-// quotient, too little to reach the next whole number.
-__device__ __forceinline__ uint32_t div_magic(int d) {
-  const int s = d > 1 ? 32 - __clz(d - 1) : 0;
-  return static_cast<uint32_t>((1ull << (31 + s)) / static_cast<uint32_t>(d)) +
-         1u;
-}
-__device__ __forceinline__ int div_by(int n, int d, uint32_t m) {
-  const int s = d > 1 ? 32 - __clz(d - 1) : 0;
-  return static_cast<int>(
-      (static_cast<uint64_t>(static_cast<uint32_t>(n)) * m) >> (31 + s));
-}
-
 struct PlanArgs {
   wan_paged_t c;
   const int32_t* new_lens;
@@ -81,6 +66,18 @@ struct PlanArgs {
   int sms;
   int few;
 };
+
+// n / d for 0 <= n < 2^31, 1 <= d <= 2^20, inv = 1 / d rounded.  The three
+// roundings of the first quotient are below 2^-22 of n / d, so with the
+// truncation what it leaves is less than 2^9 + d in size, and the second one
+// is off by at most 1.
+__device__ __forceinline__ int div_by(int n, int d, float inv) {
+  int q = static_cast<int>(static_cast<float>(n) * inv);
+  int rest = n - q * d;
+  q += static_cast<int>(static_cast<float>(rest) * inv);
+  rest = n - q * d;
+  return rest < 0 ? q - 1 : rest >= d ? q + 1 : q;
+}
 
 // Cluster barrier in two halves.
 __device__ __forceinline__ void cluster_arrive() {
@@ -117,6 +114,23 @@ __device__ __forceinline__ uint64_t block_scan(uint64_t v, uint64_t* red,
   return warp ? v + red[warp - 1] : v;
 }
 
+__device__ __forceinline__ uint64_t block_max(uint64_t v, uint64_t* red) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const uint64_t u = __shfl_xor_sync(0xffffffffu, v, o);
+    v = u > v ? u : v;
+  }
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = red[threadIdx.x & 31];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const uint64_t u = __shfl_xor_sync(0xffffffffu, v, o);
+    v = u > v ? u : v;
+  }
+  return v;
+}
+
 // First r in [0, n) with incl[r] > x (n - 1 if there is none).
 __device__ __forceinline__ int find_stream(const int* incl, int n, int x) {
   int lo = 0, hi = n - 1;
@@ -129,6 +143,9 @@ __device__ __forceinline__ int find_stream(const int* incl, int n, int x) {
   }
   return lo;
 }
+
+// Rounds of whole units beyond which the CTAs' loads count as equal.
+constexpr int kManyRounds = 16;
 
 // Scratch of build_work, one entry a stream or CTA.
 struct WorkMem {
@@ -185,22 +202,23 @@ __device__ __forceinline__ int sorted_stream(int n_streams, bool on, int nb,
                           static_cast<uint32_t>(kMaxStreams - 1 - r)
                     : 0u;
   uint32_t* s_key = reinterpret_cast<uint32_t*>(mem);
-  const int top = n_streams <= 32 ? 32 : kMaxStreams;
+  int top = 32;  // the network's size
+  while (top < n_streams) top <<= 1;
   for (int k = 2; k <= top; k <<= 1) {
     for (int j = k >> 1; j > 0; j >>= 1) {
-      uint32_t other;
       if (j >= 32) {
         __syncthreads();
         s_key[r] = key;
         __syncthreads();
-        other = s_key[r ^ j];
-      } else {
-        other = __shfl_xor_sync(0xffffffffu, key, j);
       }
-      // falling order where bit k of r is clear (up to 32 streams: in the
-      // first warp, whose bit 5 is)
-      const bool keep_max = ((r & k) == 0) == ((r & j) == 0);
-      key = keep_max ? max(key, other) : min(key, other);
+      if (r < top) {  // (whole warps)
+        const uint32_t other =
+            j >= 32 ? s_key[r ^ j] : __shfl_xor_sync(0xffffffffu, key, j);
+        // falling order where bit k of r is clear (for the last k: in all
+        // places)
+        const bool keep_max = ((r & k) == 0) == ((r & j) == 0);
+        key = keep_max ? max(key, other) : min(key, other);
+      }
     }
   }
   return kMaxStreams - 1 - static_cast<int>(key & (kMaxStreams - 1));
@@ -227,23 +245,23 @@ __device__ void build_tiles(const PlanArgs& a, int ql, int nb, uint64_t* red,
   const bool on = ql > 0;
   const bool small = a.c.n_streams <= 32;
   const int heads = a.c.heads;
-  __shared__ int s_units, s_act;
-  __shared__ unsigned long long s_top, s_sum;
+  __shared__ int s_units, s_act, s_long;
+  __shared__ unsigned long long s_sum;
   unsigned long long* s_load = mem.load;
-  const int src = sorted_stream(a.c.n_streams, on, nb, mem.a);
+  const int src =
+      a.c.n_streams > 1 ? sorted_stream(a.c.n_streams, on, nb, mem.a) : 0;
   const int n_act = __syncthreads_count(on);
   mem.a[r] = nb;
   mem.b[r] = ql;
-  if (r == 0) mem.c[0] = 0;
-  __syncthreads();
-  if (on) atomicMax(&mem.c[0], nb);
   __syncthreads();
   const bool mine = r < n_act;
   const int m_nb = mine ? mem.a[src] : 0;
   const int m_ql = mine ? mem.b[src] : 0;
   const int m_tiles = (m_ql + kTileRows - 1) / kTileRows;
   // (lengths past 65,535 blocks are scaled so that the line fits 32 bits)
-  const int down = max(0, 16 - __clz(mem.c[0]));
+  if (r == 0) s_long = m_nb;
+  __syncthreads();
+  const int down = max(0, 16 - __clz(s_long));
   const int w_nb = m_nb >> down;
   const int m_full = full_weight(w_nb), m_last = last_weight(w_nb, m_ql);
   const int units = m_tiles * heads;
@@ -275,40 +293,39 @@ __device__ void build_tiles(const PlanArgs& a, int ql, int nb, uint64_t* red,
   // Loads of the CTAs after K rounds, `share` threads a CTA; the most rounds
   // whose heaviest CTA stays within the mean, at most two fewer than there
   // are (the rounds go up and down, which leaves little beyond a unit's
-  // length between the CTAs).
-  const int share = kPlanThreads / G;
-  const int c = r % G, part = r / G;
-  auto unit_weight = [&](int u) {
-    const int i = find_stream(mem.a, n_act, u);
-    const int at = u - (i ? mem.a[i - 1] : 0);
-    return at % mem.b[i] == 0 ? mem.d[i] : mem.c[i];
-  };
+  // length between the CTAs).  After many rounds that little is not worth
+  // the sums: the loads count as equal.
   int K = U / G;
-  if (r < G) s_load[r] = 0;
-  if (r == 0) s_top = 0;
-  __syncthreads();
-  if (part < share && part < K) {
-    unsigned long long sum = 0;
-    for (int k = part; k < K; k += share)
-      sum += unit_weight(k * G + (k & 1 ? G - 1 - c : c));
-    atomicAdd(&s_load[c], sum);
-  }
-  for (int tries = 0;; ++tries) {
+  uint64_t lack = 1;
+  if (K < kManyRounds) {
+    const int share = kPlanThreads / G;
+    const int c = r % G, part = r / G;
+    auto unit_weight = [&](int u) {
+      const int i = find_stream(mem.a, n_act, u);
+      const int at = u - (i ? mem.a[i - 1] : 0);
+      return at % mem.b[i] == 0 ? mem.d[i] : mem.c[i];
+    };
+    if (r < G) s_load[r] = 0;
     __syncthreads();
-    if (r < G) atomicMax(&s_top, s_load[r]);
-    __syncthreads();
-    if (K == 0 || tries == 2 || s_top * G <= s_sum) break;
-    --K;
-    __syncthreads();
-    if (r < G)
-      s_load[r] -= unit_weight(K * G + (K & 1 ? G - 1 - r : r));
-    if (r == 0) s_top = 0;
+    if (part < share && part < K) {
+      unsigned long long sum = 0;
+      for (int k = part; k < K; k += share)
+        sum += unit_weight(k * G + (k & 1 ? G - 1 - c : c));
+      atomicAdd(&s_load[c], sum);
+    }
+    for (int tries = 0;; ++tries) {
+      __syncthreads();
+      const uint64_t top = block_max(r < G ? s_load[r] : 0, red);
+      if (K == 0 || tries == 2 || top * G <= s_sum) break;
+      --K;
+      if (r < G) s_load[r] -= unit_weight(K * G + (K & 1 ? G - 1 - r : r));
+    }
+    const uint64_t mean =
+        static_cast<uint64_t>(static_cast<double>(s_sum) / G) + 1;
+    lack = r < G && s_load[r] < mean ? mean - s_load[r] : 0;
   }
   // the line: places in proportion to what each CTA lacks
-  const uint64_t mean = (s_sum + G - 1) / G;
-  const uint64_t lack =
-      r < G && s_load[r] < mean ? mean - s_load[r] : 0;
-  const uint64_t lack_upto = block_scan(lack, red);
+  const uint64_t lack_upto = block_scan(r < G ? lack : 0, red);
   const int first = K * G;  // units before the line
   const int base = upto - units;
   // the stream's units before the line
@@ -324,13 +341,16 @@ __device__ void build_tiles(const PlanArgs& a, int ql, int nb, uint64_t* red,
   }
   __syncthreads();
   int32_t* work = a.c.work;
-  // (the line and the lacks are below 2^30: three rounds of weights)
   int* s_cut = reinterpret_cast<int*>(s_load);
   __syncthreads();
   if (r < G) {
+    // (fp32: a cut may be off by a few places, but cuts do not cross)
+    const float scale = static_cast<float>(s_line) /
+                        static_cast<float>(s_lack ? s_lack : 1);
     const int end =
         r == G - 1 ? static_cast<int>(s_line)
-                   : static_cast<int>(s_lack ? s_line * lack_upto / s_lack : 0);
+                   : min(static_cast<int>(static_cast<float>(lack_upto) * scale),
+                         static_cast<int>(s_line));
     s_cut[r + 1] = end;
     work[kLine + r + 1] = end;
     if (r == 0) s_cut[0] = work[kLine] = 0;
@@ -410,12 +430,12 @@ __global__ void __launch_bounds__(kPlanThreads)
   __shared__ int s_need[kMaxStreams];   // pages going out, inclusive
   __shared__ int s_old[kMaxStreams];    // tokens before the step
   __shared__ int s_from[kMaxStreams];   // first page coming back
-  // tokens of a frame and of a row, with their div_magic
+  // tokens of a frame and of a row, and one over them
   __shared__ __align__(8) int s_dims[2 * kMaxStreams];
   int* s_hw = s_dims;
   int* s_w = s_dims + kMaxStreams;
-  __shared__ uint32_t s_mhw[kMaxStreams];
-  __shared__ __align__(8) uint32_t s_mw[kMaxStreams];
+  __shared__ float s_inv_hw[kMaxStreams];
+  __shared__ __align__(8) float s_inv_w[kMaxStreams];
   const wan_paged_t& c = a.c;
   const int R = c.n_streams;
   const int r = threadIdx.x;
@@ -476,8 +496,8 @@ __global__ void __launch_bounds__(kPlanThreads)
   if (admit) {  // H and W lie in the grid, so H W <= 2^20
     s_hw[r] = cfg.x * cfg.y;
     s_w[r] = cfg.y;
-    s_mhw[r] = div_magic(cfg.x * cfg.y);
-    s_mw[r] = div_magic(cfg.y);
+    s_inv_hw[r] = 1.0f / static_cast<float>(cfg.x * cfg.y);
+    s_inv_w[r] = 1.0f / static_cast<float>(cfg.y);
   }
   // admission stops for good at the first stream that does not fit, so the
   // admitted needs are a prefix of the line of needs
@@ -490,9 +510,9 @@ __global__ void __launch_bounds__(kPlanThreads)
                        s_from,
                        s_rows,
                        s_old,
-                       reinterpret_cast<int*>(s_mhw),
+                       reinterpret_cast<int*>(s_inv_hw),
                        s_end,
-                       reinterpret_cast<unsigned long long*>(s_mw),
+                       reinterpret_cast<unsigned long long*>(s_inv_w),
                        reinterpret_cast<int64_t*>(s_dims)};
   const int kv = ended ? 0 : old + (admit ? rows : 0);
   const int ctas = gridDim.x;
@@ -551,7 +571,7 @@ __global__ void __launch_bounds__(kPlanThreads)
   // The tokens' records: the page of a new position is either one the stream
   // held (its table entry does not change) or comes from the ring.  A warp
   // takes consecutive records, so that its stream moves on by a step or two
-  // between them; divisions by a stream's frame and row are multiplications.
+  // between them; divisions by a stream's frame and row are products.
   int4* tok = reinterpret_cast<int4*>(c.tokens);
   const int n_rows = s_end[R - 1];
   const int warps = movers * (kPlanThreads / 32);
@@ -568,9 +588,9 @@ __global__ void __launch_bounds__(kPlanThreads)
       const int off = i - (q ? s_end[q - 1] : 0);
       if (off < s_rows[q]) {
         const int pos = s_old[q] + off;
-        rec.x = div_by(pos, s_hw[q], s_mhw[q]);
+        rec.x = div_by(pos, s_hw[q], s_inv_hw[q]);
         const int rest = pos - rec.x * s_hw[q];
-        rec.y = div_by(rest, s_w[q], s_mw[q]);
+        rec.y = div_by(rest, s_w[q], s_inv_w[q]);
         rec.z = rest - rec.y * s_w[q];
         const int p = pos >> a.page_shift;
         const int h0 = (s_old[q] + ps - 1) >> a.page_shift;

@@ -30,11 +30,14 @@ constexpr int kTileRows = 256;
 constexpr int kFewCtasPerSm = 2;
 constexpr int kMaxCtas = 511;
 
-// Weight of a unit: 8 a 128-key block with two row tiles, 5 with one, and
-// kUnitWeight for its start and end (measured: see build_tiles).
+// Weight of a unit: 8 a 128-key block with two row tiles, 6 with one, and
+// kUnitWeight for its start and end.  Measured with one-tile weights of 4, 5
+// and 6: 816, 771 and 749 us for 4,680 rows x 12 heads over 32,760 keys, 100,
+// 92 and 88 us for 20 to 400 rows of six streams; starts of 24, 48 and 96:
+// 91.5, 89.0 and 88.3 us for the latter.
 constexpr int kPairWeight = 8;
-constexpr int kOneWeight = 5;
-constexpr int kUnitWeight = 24;
+constexpr int kOneWeight = 6;
+constexpr int kUnitWeight = 48;
 
 // work: a header, LINE[0 .. kMaxCtas], kJoinInts ints per unit of the line
 // (at most three rounds of them), then kEnt ints per active stream.
@@ -100,7 +103,7 @@ struct Line {
 
 // First key that the query at position a sees, and one past its last.
 __host__ __device__ __forceinline__ int64_t chunk_end(int a, int chunk) {
-  return (static_cast<int64_t>(a) / chunk + 1) * chunk;
+  return (static_cast<int64_t>(a / chunk) + 1) * chunk;
 }
 __host__ __device__ __forceinline__ int key_lo(int a, int chunk, int window) {
   if (window <= 0) return 0;

@@ -42,7 +42,7 @@ class PagedCache:
     max_pages: block table entries a stream can use, evicted ones included.
     token_cap: packed rows of q, k, v and o.  max_new: most new tokens of
     one stream in a step (default token_cap); together with heads / kv_heads
-    it picks the attention kernel.
+    it picks the attention kernel (max_new may be set anew before a plan).
 
     state holds everything that a plan carries from step to step in one
     int32 tensor, with the views kv_lens, first_pages, block_table, free_ring
@@ -109,7 +109,7 @@ class PagedCache:
         if self._table_bytes == 0:
             raise ValueError("grid %r has no RoPE table" % (grid,))
         self._desc = None
-        self._workspace = self._need_for = None
+        self._workspace = self._need_for = self._planned = None
         self._q_shape = torch.Size((self.token_cap, self.heads, 128))
         self._kv_shape = torch.Size((self.token_cap, self.kv_heads, 128))
         self._pool_shape = torch.Size((self.n_pages, self.kv_heads,
@@ -183,6 +183,7 @@ class PagedCache:
         if new_lens.get_device() != self._index:
             wan._on_cuda(("streams", self.streams), ("new_lens", new_lens))
         wan.paged_plan(self.descriptor(), new_lens, stream=stream)
+        self._planned = self.max_new
 
     def write(self, q, k, v, wq, wk, table, k_pages, v_pages, q_out=None,
               eps=1e-6, stream=None):
@@ -232,6 +233,9 @@ class PagedCache:
         self._check(self._q_shape, "o", o)
         self._check(self._pool_shape, "k_pages", k_pages)
         self._check(self._pool_shape, "v_pages", v_pages)
+        if self._planned != self.max_new:
+            # the plan divided the work for the kernel max_new picks
+            raise ValueError("attn needs a plan made with the same max_new")
         if workspace is None:
             workspace = self.workspace()
         else:
