@@ -364,6 +364,7 @@ __device__ void build_tiles(const PlanArgs& a, int ql, int nb, uint64_t* red,
     e[E_LAST] = m_last;
     const int64_t start = static_cast<int64_t>(line_upto - on_line) -
                           static_cast<int64_t>(skipped);
+    e[E_FIRST] = static_cast<int>(line_upto - on_line);
     *reinterpret_cast<int64_t*>(e + E_LINE) = start;
     mem.e[r] = src;
     mem.f[r] = m_ql;
@@ -633,7 +634,8 @@ struct WriteArgs {
   const float4* w[2];      // weights of q and k
   const float4* table;     // RoPE rows of 11 float4
   const int4* tokens;
-  int rows;                // packed rows
+  const int32_t* n_rows;   // packed rows of the streams (q_start[R])
+  int rows;                // packed rows of the tensors
   int heads, kv_heads;
   int F, H, W;
   int page_shift;
@@ -659,17 +661,24 @@ __launch_bounds__(kWrThreads, kRows ? wr_min_blocks<kRows>() : 8)
   const int which = static_cast<int>(it - 3u * row);
   if (row < a.rows) {
     const int4 tk = __ldg(a.tokens + row);
-    // rows of no stream, and records that no plan writes
-    if (tk.w < 0 || tk.w >= a.slots || static_cast<unsigned>(tk.x) >= a.F ||
-        static_cast<unsigned>(tk.y) >= a.H ||
-        static_cast<unsigned>(tk.z) >= a.W)
-      return;
+    if (row >= __ldg(a.n_rows)) return;  // behind the last stream
     const int nh = which == 0 ? a.heads : a.kv_heads;
     // selects, not indexes: a runtime index into the parameters would copy
     // them to the stack
     const uint4* in = which == 0 ? a.in[0] : which == 1 ? a.in[1] : a.in[2];
     uint4* out = which == 0 ? a.out[0] : which == 1 ? a.out[1] : a.out[2];
     in += static_cast<int64_t>(row) * nh * 16 + c;
+    uint4 x[kRows ? kRows : 1];
+    if (kRows) {
+#pragma unroll
+      for (int k = 0; k < kRows; ++k)
+        if (hsub + 2 * k < nh) x[k] = in[(hsub + 2 * k) * 16];
+    }
+    // records that no plan writes, rows of refused streams
+    if (tk.w < 0 || tk.w >= a.slots || static_cast<unsigned>(tk.x) >= a.F ||
+        static_cast<unsigned>(tk.y) >= a.H ||
+        static_cast<unsigned>(tk.z) >= a.W)
+      return;
     int64_t hstep = 16;  // uint4 from one head's row to the next
     if (which == 0) {
       out += static_cast<int64_t>(row) * nh * 16 + c;
@@ -679,7 +688,6 @@ __launch_bounds__(kWrThreads, kRows ? wr_min_blocks<kRows>() : 8)
       hstep = 16ll << a.page_shift;
       out += static_cast<int64_t>(page) * nh * hstep + off * 16 + c;
     }
-    uint4 x[kRows ? kRows : 1];
     float ss = 0.f;
     auto squares = [&](const uint4& v) {
       const uint32_t vv[4] = {v.x, v.y, v.z, v.w};
@@ -689,11 +697,6 @@ __launch_bounds__(kWrThreads, kRows ? wr_min_blocks<kRows>() : 8)
         ss = fmaf(f.x, f.x, fmaf(f.y, f.y, ss));
       }
     };
-    if (kRows) {
-#pragma unroll
-      for (int k = 0; k < kRows; ++k)
-        if (hsub + 2 * k < nh) x[k] = in[(hsub + 2 * k) * 16];
-    }
     if (which == 2) {
       if (kRows) {
 #pragma unroll
@@ -867,6 +870,7 @@ int wan_paged_write(const wan_paged_t* c, const void* q, void* q_out,
   a.w[1] = reinterpret_cast<const float4*>(wk);
   a.table = static_cast<const float4*>(d_table);
   a.tokens = reinterpret_cast<const int4*>(c->tokens);
+  a.n_rows = c->q_start + c->n_streams;
   a.rows = c->token_cap;
   a.heads = c->heads;
   a.kv_heads = c->kv_heads;

@@ -73,6 +73,7 @@ enum : int {
   // kTile
   E_FULL = 3,     // weight of a unit with two row tiles
   E_LAST = 4,     // weight of a unit of the last tile pair
+  E_FIRST = 5,    // the line's place at which those on it start
   E_LINE = 6      // (64 bits) the line's place at which the stream's units
                   // would start, had all of them been on it
 };

@@ -44,19 +44,28 @@ __device__ __forceinline__ int page_of(const PagedArgs& a, int stream,
   return page >= 0 && page < a.c.n_pages ? page : a.c.n_pages;
 }
 
-// Last entry of the work list whose field f is <= x.
+// Last entry of the work list whose field f, times mul, is <= x (the first
+// one's is 0).  By the whole warp, with the same x: one round of loads for up
+// to 32 entries, two for the rest.
 __device__ __forceinline__ const int32_t* find_entry(const int32_t* work,
-                                                     int f, int64_t mul,
-                                                     int64_t x) {
-  int lo = 0, hi = __ldg(work + pg::H_ACTIVE) - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (__ldg(work + pg::kHdr + pg::kEnt * mid + f) * mul <= x)
-      lo = mid;
-    else
-      hi = mid - 1;
+                                                     int n, int f, int mul,
+                                                     int x) {
+  const int32_t* list = work + pg::kHdr;
+  if (n <= 1) return list;
+  const int lane = threadIdx.x & 31;
+  const int step = (n + 31) >> 5;
+  int i = lane * step;
+  unsigned at = __ballot_sync(
+      0xffffffffu, i < n && __ldg(list + pg::kEnt * i + f) * mul <= x);
+  int first = (31 - __clz(at)) * step;
+  if (step > 1) {
+    i = first + lane;
+    at = __ballot_sync(0xffffffffu, lane < step && i < n &&
+                                        __ldg(list + pg::kEnt * i + f) * mul <=
+                                            x);
+    first += 31 - __clz(at);
   }
-  return work + pg::kHdr + pg::kEnt * lo;
+  return list + pg::kEnt * first;
 }
 
 // Keys of a stream that its table can hold.
@@ -176,11 +185,11 @@ struct Segment {
 };
 
 // The part of an item that starts at x, up to x1 on the line.
-__device__ __forceinline__ Segment segment_at(const PagedArgs& a, int x,
-                                              int x1) {
+__device__ __forceinline__ Segment segment_at(const PagedArgs& a, int active,
+                                              int x, int x1) {
   Segment s;
   const int4* e = reinterpret_cast<const int4*>(
-      find_entry(a.c.work, pg::E_BASE, a.c.kv_heads, x));
+      find_entry(a.c.work, active, pg::E_BASE, a.c.kv_heads, x));
   const int4 e0 = __ldg(e), e1 = __ldg(e + 1);
   s.stream = e0.x;
   const int n = e0.z;
@@ -249,12 +258,12 @@ __global__ void __launch_bounds__(kThreads, pg::kFewCtasPerSm)
                      const __grid_constant__ PagedArgs args) {
   extern __shared__ __align__(128) uint8_t smem_raw[];
   const int32_t* work = args.c.work;
-  const int ctas = __ldg(work + pg::H_CTAS);
+  // {H_MODE, H_ACTIVE, H_TOTAL, H_CTAS}
+  const int4 hdr = __ldg(reinterpret_cast<const int4*>(work));
   const int cta = blockIdx.x;
-  if (__ldg(work + pg::H_MODE) != pg::kModeFew || cta >= ctas ||
-      __ldg(work + pg::H_ACTIVE) < 1)
-    return;
-  const pg::Line line(__ldg(work + pg::H_TOTAL), ctas);
+  if (hdr.x != pg::kModeFew || hdr.y < 1 || cta >= hdr.w) return;
+  const int active = hdr.y;
+  const pg::Line line(hdr.z, hdr.w);
   const int x0 = line.first(cta), x1 = line.first(cta + 1);
   launch_dependents();
   const int warp = threadIdx.x >> 5;
@@ -268,7 +277,7 @@ __global__ void __launch_bounds__(kThreads, pg::kFewCtasPerSm)
   const int64_t page_bytes = head_bytes * args.c.kv_heads;
 
   // The loading side: stage lj of segment ls is the next one to fetch.
-  Segment ls = segment_at(args, x0, x1);
+  Segment ls = segment_at(args, active, x0, x1);
   int lx = x0;
   int lj = 0, lg = 0;
   int lpage = page_of(args, ls.stream,
@@ -302,7 +311,7 @@ __global__ void __launch_bounds__(kThreads, pg::kFewCtasPerSm)
       if (++lj == ls.n) {
         lx += ls.n;
         lj = 0;
-        if (lx < x1) ls = segment_at(args, lx, x1);
+        if (lx < x1) ls = segment_at(args, active, lx, x1);
       }
       // the next fetch's page arrives while this stage is computed
       if (lg < total_stages)
@@ -320,7 +329,7 @@ __global__ void __launch_bounds__(kThreads, pg::kFewCtasPerSm)
   const int gr = lane >> 2, t4 = lane & 3;
   int g = 0;
   for (int x = x0; x < x1;) {
-    const Segment s = segment_at(args, x, x1);
+    const Segment s = segment_at(args, active, x, x1);
     const int4 cfg =
         __ldg(reinterpret_cast<const int4*>(args.c.streams) + s.stream);
     const int chunk = cfg.z, window = cfg.w;
@@ -662,6 +671,7 @@ __device__ __forceinline__ bool unit_at(const PagedArgs& a, const Walk& w,
                                         Unit& t) {
   const int32_t* work = a.c.work;
   const int32_t* e;
+  const int active = __ldg(work + pg::H_ACTIVE);
   int local, s0 = 0, s1 = 1, weight = 1;
   t.slot = -1;
   t.span = 0;
@@ -669,34 +679,14 @@ __device__ __forceinline__ bool unit_at(const PagedArgs& a, const Walk& w,
     const int ctas = __ldg(work + pg::H_CTAS);
     const int c = blockIdx.x;
     const int u = w.k * ctas + (w.k & 1 ? ctas - 1 - c : c);
-    e = find_entry(work, pg::E_BASE, 1, u);
+    e = find_entry(work, active, pg::E_BASE, 1, u);
     local = u - __ldg(e + pg::E_BASE);
   } else {
     const int x0 = __ldg(work + pg::kLine + blockIdx.x);
     const int x1 = __ldg(work + pg::kLine + blockIdx.x + 1);
     if (w.x >= x1) return false;
     // the stream whose units hold place x, and the place among them
-    const int32_t* base = work + pg::kHdr;
-    int lo = 0, hi = __ldg(work + pg::H_ACTIVE) - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      const int32_t* m = base + pg::kEnt * mid;
-      const int64_t line =
-          __ldg(reinterpret_cast<const long long*>(m + pg::E_LINE));
-      // a stream's first place: units of earlier rounds are not on the line
-      const int skip = min(max(__ldg(work + pg::H_WAVES) *
-                                       __ldg(work + pg::H_CTAS) -
-                                   __ldg(m + pg::E_BASE),
-                               0),
-                           __ldg(m + pg::E_COUNT) * a.c.heads);
-      if (line + pg::weight_before(skip, __ldg(m + pg::E_COUNT),
-                               __ldg(m + pg::E_FULL),
-                               __ldg(m + pg::E_LAST)) <= w.x)
-        lo = mid;
-      else
-        hi = mid - 1;
-    }
-    e = base + pg::kEnt * lo;
+    e = find_entry(work, active, pg::E_FIRST, 1, w.x);
     const int tiles = __ldg(e + pg::E_COUNT);
     const int full = __ldg(e + pg::E_FULL), last = __ldg(e + pg::E_LAST);
     const int64_t y =
