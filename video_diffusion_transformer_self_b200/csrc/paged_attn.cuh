@@ -174,7 +174,8 @@ constexpr int kKeys = pg::kStage / kWarps;     // keys of a warp's part: 16
 constexpr uint32_t kPart = kKeys * HD * 2;     // its K (or V): 4 KB
 constexpr uint32_t kWarpRing = kDepth * 2 * kPart;
 constexpr int kRows = pg::kFewRows;
-constexpr uint32_t kJoinFloats = kRows * HD + 2 * kRows;
+constexpr int kJoinRow = HD + 4;  // floats; the pad spreads rows over banks
+constexpr uint32_t kJoinFloats = kRows * kJoinRow + 2 * kRows;
 constexpr uint32_t kSmem = kWarps * kWarpRing + 2 * kJoinFloats * 4;
 static_assert(kKeys == 16, "one k-step of P V, and never two pages");
 
@@ -280,15 +281,21 @@ __global__ void __launch_bounds__(kThreads, pg::kFewCtasPerSm)
   Segment ls = segment_at(args, active, x0, x1);
   int lx = x0;
   int lj = 0, lg = 0;
-  int lpage = page_of(args, ls.stream,
-                      static_cast<int64_t>(ls.stage0) * pg::kStage +
-                          warp * kKeys);
+  // pages of this warp's part of the segment's stages, 32 at a time (one a
+  // lane: a read a stage sat between the fetches)
+  auto pages_from = [&](int j) {
+    return page_of(args, ls.stream,
+                   static_cast<int64_t>(ls.stage0 + j + lane) * pg::kStage +
+                       warp * kKeys);
+  };
+  int pages = pages_from(0);
   const int total_stages = x1 - x0;
   const uint32_t dst0 = swz(lane >> 4, lane & 15);
   auto fetch = [&]() {
     if (lg < total_stages) {
       const int64_t pos =
           static_cast<int64_t>(ls.stage0 + lj) * pg::kStage + warp * kKeys;
+      const int lpage = __shfl_sync(0xffffffffu, pages, lj & 31);
       const bool live = lpage < args.c.n_pages;
       const int64_t off =
           (live ? lpage * page_bytes + ls.head * head_bytes +
@@ -311,34 +318,28 @@ __global__ void __launch_bounds__(kThreads, pg::kFewCtasPerSm)
       if (++lj == ls.n) {
         lx += ls.n;
         lj = 0;
-        if (lx < x1) ls = segment_at(args, active, lx, x1);
+        if (lx < x1) {
+          ls = segment_at(args, active, lx, x1);
+          pages = pages_from(0);
+        }
+      } else if ((lj & 31) == 0) {
+        pages = pages_from(lj);
       }
-      // the next fetch's page arrives while this stage is computed
-      if (lg < total_stages)
-        lpage = page_of(args, ls.stream,
-                        static_cast<int64_t>(ls.stage0 + lj) * pg::kStage +
-                            warp * kKeys);
     }
     cp_async_commit();  // an empty group keeps the count
   };
-#pragma unroll
-  for (int i = 0; i < kDepth - 1; ++i) fetch();
-
   // Fragments of m16n8k16: thread (gr, t4) = (lane / 4, lane % 4) holds rows
   // gr and gr + 8, columns 2 t4, 2 t4 + 1 (+ 8) of A and of the results.
   const int gr = lane >> 2, t4 = lane & 3;
-  int g = 0;
-  for (int x = x0; x < x1;) {
-    const Segment s = segment_at(args, active, x, x1);
+  // rows gr and gr + 8 of a segment: row r is query head head * group +
+  // r % group of new token r / group
+  uint32_t qf[8][4];
+  int lo[2], hi[2], item_lo;
+  int64_t orow[2];
+  auto load_rows = [&](const Segment& s) {
     const int4 cfg =
         __ldg(reinterpret_cast<const int4*>(args.c.streams) + s.stream);
-    const int chunk = cfg.z, window = cfg.w;
     const int rows = min(s.ql * args.group, kRows);
-    // rows gr and gr + 8: row r is query head head * group + r % group of
-    // new token r / group
-    uint32_t qf[8][4];
-    int lo[2], hi[2];
-    int64_t orow[2];
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int r = gr + 8 * e;
@@ -347,10 +348,6 @@ __global__ void __launch_bounds__(kThreads, pg::kFewCtasPerSm)
                 s.head * args.group + (r - i * args.group);
       const bool on = r < rows && s.q0 + i < args.c.token_cap;
       if (!on) orow[e] = -1;
-      const int a = s.kv - s.ql + i;
-      // a row of padding takes part unmasked and is never written
-      lo[e] = on ? pg::key_lo(max(a, 0), chunk, window) : 0;
-      hi[e] = on ? pg::key_hi(a, chunk, s.kv) : INT32_MAX;
       const uint32_t* src = reinterpret_cast<const uint32_t*>(
           args.q + (on ? orow[e] : 0) * HD);
 #pragma unroll
@@ -358,8 +355,21 @@ __global__ void __launch_bounds__(kThreads, pg::kFewCtasPerSm)
         qf[k][e] = on ? __ldg(src + k * 8 + t4) : 0u;
         qf[k][2 + e] = on ? __ldg(src + k * 8 + 4 + t4) : 0u;
       }
+      // a row of padding takes part unmasked and is never written
+      const int a = s.kv - s.ql + i;
+      lo[e] = on ? pg::key_lo(max(a, 0), cfg.z, cfg.w) : 0;
+      hi[e] = on ? pg::key_hi(a, cfg.z, s.kv) : INT32_MAX;
     }
-    const int item_lo = pg::key_lo(max(s.kv - s.ql, 0), chunk, window);
+    item_lo = pg::key_lo(max(s.kv - s.ql, 0), cfg.z, cfg.w);
+  };
+  // the first rows' reads are under way before the first fetches wait for
+  // their pages
+  Segment s = ls;
+  load_rows(s);
+#pragma unroll
+  for (int i = 0; i < kDepth - 1; ++i) fetch();
+  int g = 0;
+  for (int x = x0;;) {
     float o[16][4];
 #pragma unroll
     for (int d = 0; d < 16; ++d)
@@ -485,12 +495,12 @@ __global__ void __launch_bounds__(kThreads, pg::kFewCtasPerSm)
       for (int e = 0; e < 2; ++e) {
         const int r = gr + 8 * e;
         if (t4 == 0) {
-          dst[kRows * HD + r] = m[e];
-          dst[kRows * HD + kRows + r] = l[e];
+          dst[kRows * kJoinRow + r] = m[e];
+          dst[kRows * kJoinRow + kRows + r] = l[e];
         }
 #pragma unroll
         for (int d = 0; d < 16; ++d)
-          *reinterpret_cast<float2*>(dst + r * HD + d * 8 + 2 * t4) =
+          *reinterpret_cast<float2*>(dst + r * kJoinRow + d * 8 + 2 * t4) =
               make_float2(o[d][2 * e], o[d][2 * e + 1]);
       }
     };
@@ -498,16 +508,16 @@ __global__ void __launch_bounds__(kThreads, pg::kFewCtasPerSm)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int r = gr + 8 * e;
-        const float m2 = src[kRows * HD + r];
+        const float m2 = src[kRows * kJoinRow + r];
         const float mn = fmaxf(m[e], m2);
         const float w1 = m[e] == -INFINITY ? 0.f : ex2(m[e] - mn);
         const float w2 = m2 == -INFINITY ? 0.f : ex2(m2 - mn);
-        l[e] = l[e] * w1 + src[kRows * HD + kRows + r] * w2;
+        l[e] = l[e] * w1 + src[kRows * kJoinRow + kRows + r] * w2;
         m[e] = mn;
 #pragma unroll
         for (int d = 0; d < 16; ++d) {
-          const float2 v = *reinterpret_cast<const float2*>(src + r * HD +
-                                                            d * 8 + 2 * t4);
+          const float2 v = *reinterpret_cast<const float2*>(src + r * kJoinRow + d * 8 +
+                                              2 * t4);
           o[d][2 * e] = fmaf(v.x, w2, o[d][2 * e] * w1);
           o[d][2 * e + 1] = fmaf(v.y, w2, o[d][2 * e + 1] * w1);
         }
@@ -551,6 +561,9 @@ __global__ void __launch_bounds__(kThreads, pg::kFewCtasPerSm)
       }
     }
     x += s.n;
+    if (x >= x1) break;
+    s = segment_at(args, active, x, x1);
+    load_rows(s);
   }
 }
 
