@@ -291,8 +291,9 @@ int wan_attn_pair_resident_clusters(void);
  * resolutions: their keys and values live in pages of one pool, found
  * through a block table per stream, and every length stays on the device,
  * so a step can be captured into a CUDA graph and replayed with other
- * lengths.  A step is one wan_paged_plan, then for every layer (and every
- * denoising pass over the same chunk) wan_paged_write and wan_paged_attn.
+ * lengths (after a first call of each kind outside the capture).  A step is
+ * one wan_paged_plan, then for every layer (and every denoising pass over
+ * the same chunk) wan_paged_write and wan_paged_attn.
  * The pages have no counterpart of the paging itself; what the attention
  * sees is wan_block_causal_attn's rule plus the window.
  *
@@ -377,10 +378,10 @@ int wan_paged_plan(const wan_paged_t* c, const int32_t* new_lens, void* s);
  * and k (mean over kv_heads * 128, weights wk, result to its slot in
  * k_pages); v goes to its slot in v_pages unchanged.  The rotation is that
  * of wan_qk_norm_rope at the row's (t, h, w), with the table of c->grid.
- * Only c->tokens is read of the plan: a row whose slot is not in
- * [0, n_pages * page_size) or whose position is outside the grid is left
- * out (its q_out row stays as it was).  The slots of a call must differ.
- * q, k and v must not overlap the pools.                                   */
+ * Of the plan, tokens and q_start[R] are read: a row from q_start[R] on, or
+ * whose slot is not in [0, n_pages * page_size), or whose position is
+ * outside the grid, is left out (its q_out row stays as it was).  The slots
+ * of a call must differ.  q, k and v must not overlap the pools.           */
 int wan_paged_write(const wan_paged_t* c, const void* q, void* q_out,
                     const void* k, const void* v, const float* wq,
                     const float* wk, void* k_pages, void* v_pages,

@@ -182,7 +182,10 @@ __device__ void build_few(const PlanArgs& a, int ql, int kv, int q0, int lo,
   }
   if (r == blockDim.x - 1) {
     const int64_t total = static_cast<int64_t>(base + n) * a.c.kv_heads;
-    const int64_t most = static_cast<int64_t>(a.sms) * kFewCtasPerSm;
+    // a stage each up to one CTA an SM, then two (12 heads over 2,000 keys,
+    // 384 stages: 8.3 us on 192 CTAs, 9.0 on 296)
+    const int64_t most = min(max(total / 2, static_cast<int64_t>(a.sms)),
+                             static_cast<int64_t>(a.sms) * kFewCtasPerSm);
     work[H_MODE] = kModeFew;
     work[H_ACTIVE] = idx + on;
     work[H_TOTAL] = static_cast<int>(total);

@@ -14,7 +14,8 @@ pages -- on the device and runs the three calls of a step on it::
 The page pools belong to the caller, one pair per layer (``new_pools``); all
 layers share the tables.  The layouts and rules are those of include/wan.h.
 No call synchronises; everything a step needs is on the device, so a step can
-be captured into a CUDA graph and replayed after new_lens was overwritten.
+be captured into a CUDA graph (after a first one outside the capture) and
+replayed after new_lens was overwritten.
 """
 
 import math
@@ -115,6 +116,7 @@ class PagedCache:
         self._pool_shape = torch.Size((self.n_pages, self.kv_heads,
                                        self.page_size, 128))
         self.reset()
+        self.workspace()  # not inside a first call that is being captured
 
     def reset(self):
         """All streams empty, all pages free."""
@@ -216,9 +218,9 @@ class PagedCache:
         return self._need
 
     def workspace(self):
-        """The cache's own scratch, allocated on first use.  Calls that
-        overlap on the device need one each (``attn``'s workspace
-        argument)."""
+        """The cache's own scratch (allocated anew if another max_new needs
+        more).  Calls that overlap on the device need one each (``attn``'s
+        workspace argument)."""
         need = self.workspace_bytes()
         if self._workspace is None or self._workspace.numel() < need:
             self._workspace = torch.empty(need, dtype=torch.uint8,
