@@ -623,11 +623,14 @@ __global__ void __launch_bounds__(kPlanThreads)
 // independent loads, one reduction and one batch of stores; a head's 256
 // bytes land contiguously in its page.  For more than 2 * 20 heads the row
 // is read twice (the second time from L2).  One item a warp and as many CTAs
-// as that takes: new CTAs load while others store, where a warp that walked
-// several items alternated between the two (43,200 rows x 40 heads, 2.65 GB:
-// 446 us walking, 414 us so, 6.4 TB/s; 3 CTAs an SM instead of 4: 499 us;
-// 4,680 rows x 12 heads: 14.5 us at 7 CTAs an SM, 15.8 at 6).
-constexpr int kWrThreads = 128;
+// as that takes, two warps each: new CTAs load while others store, where a
+// warp that walked several items alternated between the two.  43,200 rows x
+// 40 heads, 2.65 GB: 398 us, 6.7 TB/s (4-warp CTAs 403, walking 446; 12 warps
+// an SM instead of 16: 499 us).  4,680 rows x 12 heads, 86 MB: 14.4 us out of
+// L2, 20.4 after other traffic (a plain copy of as much: 9.5 and 15.4), bound
+// by the latency of a warp's chain (record, row, weights) over 3.3 rounds of
+// CTAs.
+constexpr int kWrThreads = 64;
 constexpr int kWrWarps = kWrThreads / 32;
 constexpr int kWrMaxRows = 20;
 
@@ -646,15 +649,21 @@ struct WriteArgs {
   float eps;
 };
 
+// resident CTAs an SM that each row-register budget allows
 template <int kRows>
 constexpr int wr_min_blocks() {
-  return kRows <= 4 ? 9 : kRows <= 8 ? 7 : kRows <= 12 ? 6 : 4;
+  return kRows == 0   ? 16
+         : kRows <= 4 ? 18
+         : kRows <= 6 ? 16
+         : kRows <= 8 ? 14
+         : kRows <= 12 ? 12
+                       : 8;
 }
 
 // kRows 0: any head count, two passes over the row.
 template <int kRows>
 __global__ void
-__launch_bounds__(kWrThreads, kRows ? wr_min_blocks<kRows>() : 8)
+__launch_bounds__(kWrThreads, wr_min_blocks<kRows>())
     paged_write_kernel(const __grid_constant__ WriteArgs a) {
   const int lane = threadIdx.x & 31;
   const int c = lane & 15;
@@ -885,6 +894,7 @@ int wan_paged_write(const wan_paged_t* c, const void* q, void* q_out,
   a.eps = eps;
   void (*kern)(WriteArgs) =
       c->heads <= 8    ? paged_write_kernel<4>
+      : c->heads <= 12 ? paged_write_kernel<6>
       : c->heads <= 16 ? paged_write_kernel<8>
       : c->heads <= 24 ? paged_write_kernel<12>
       : c->heads <= 2 * kWrMaxRows
