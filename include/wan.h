@@ -370,7 +370,9 @@ size_t wan_paged_work_bytes(int n_streams);
  * free_ring, ring_state, q_start, q_lens, status, tokens (all token_cap of
  * them) and work.  A free ring starts as pages 0 .. n_pages - 1 with
  * ring_state {0, n_pages}, lengths and first pages 0, table entries -1.
- * One launch; plans of one cache must not overlap on the device.           */
+ * One launch.  A plan must not overlap on the device with another plan of
+ * the cache or with calls that use the one before; all calls of a step take
+ * the descriptor that the plan was made with.                              */
 int wan_paged_plan(const wan_paged_t* c, const int32_t* new_lens, void* s);
 
 /* Writes the planned tokens: t <- rope3d(t / sqrt(mean(t^2) + eps) * w) for
@@ -395,9 +397,10 @@ int wan_paged_write(const wan_paged_t* c, const void* q, void* q_out,
  * the stream's end, or before its window) may hold anything, NaN included.
  * fp32 softmax and accumulation; the weights are rounded to bf16 for the
  * tensor cores.  o must not alias q or the pools.
- * workspace: wan_paged_workspace_bytes(c) bytes of device memory, 16-byte
- * aligned, contents free on entry and unspecified on return; calls that
- * share one must not overlap on the device.                                */
+ * workspace: wan_paged_workspace_bytes(c) bytes of device memory (of the
+ * current device; WAN_ENOSPACE if there are fewer), 16-byte aligned,
+ * contents free on entry and unspecified on return; calls that share one
+ * must not overlap on the device.  Two launches.                           */
 size_t wan_paged_workspace_bytes(const wan_paged_t* c);
 int wan_paged_attn(const wan_paged_t* c, const void* q, const void* k_pages,
                    const void* v_pages, void* o, float softmax_scale,

@@ -362,3 +362,43 @@ def test_random_streams(seed):
     _run(streams, (400, 4, 5), ps, kv_heads * group, kv_heads, steps,
          3000 + seed, max_new, 40 * R + 100,
          check=(1, len(steps) - 2, len(steps) - 1))
+
+
+@pytest.mark.parametrize("max_new", [16, 300])
+def test_pools_past_32_bit_offsets(max_new):
+    # K and V pools of 2.3e9 elements each, the stream's pages at their end
+    # (and one at the front)
+    ps, kv_heads, n_pages = 128, 8, 17600
+    assert n_pages * ps * kv_heads * 128 > 2 ** 31
+    c, oc = make([(8, 8, 64, 0)], (20, 8, 8), n_pages, ps, 10, 8, kv_heads,
+                 300, max_new)
+    oc.ring = [n_pages - 1, 0] + list(range(n_pages - 2, 0, -1))
+    c.free_ring.copy_(torch.tensor(oc.ring, dtype=torch.int32))
+    kp, vp = c.new_pools()
+    w = torch.ones(kv_heads * 128, device="cuda")
+    table = wan.rope3d_table(c.grid)
+    keys = torch.zeros(0, kv_heads, 128, dtype=torch.bfloat16)
+    vals = keys
+    for i, n in enumerate([max_new] * (320 // max_new) + [7]):
+        want = step(c, oc, [n])
+        q, k, v = (rows_bf16(300, 8, 40 + 3 * i + j).cuda() for j in range(3))
+        c.write(q, k, v, w, w, table, kp, vp)
+        o = torch.zeros_like(q)
+        c.attn(q, kp, vp, o)
+        slots = c.tokens[:n, 3].cpu().long()
+        assert int(slots.max()) >= (n_pages - 9) * ps or int(
+            slots.max()) < 128
+        page, off = slots.cuda() // ps, slots.cuda() % ps
+        keys = torch.cat([keys, kp[page, :, off].cpu()])
+        vals = torch.cat([vals, vp[page, :, off].cpu()])
+        assert torch.equal(vals[-n:], v[:n].cpu())
+    torch.cuda.synchronize()
+    s = np.einsum("ihd,jhd->hij", f64(q)[:7], f64(keys)) * SCALE
+    a = np.arange(oc.kv[0] - 7, oc.kv[0])[:, None]
+    j = np.arange(oc.kv[0])[None]
+    s = np.where(j < (a // 64 + 1) * 64, s, -np.inf)
+    p = np.exp(s - s.max(-1, keepdims=True))
+    p /= p.sum(-1, keepdims=True)
+    ref = np.einsum("hij,jhd->ihd", p, f64(vals))
+    mag = np.einsum("hij,jhd->ihd", p, np.abs(f64(vals)))
+    assert_attn(f64(o)[:7], ref, mag, "large pool", 40.0)

@@ -120,6 +120,7 @@ __device__ __forceinline__ uint64_t block_max(uint64_t v, uint64_t* red) {
     const uint64_t u = __shfl_xor_sync(0xffffffffu, v, o);
     v = u > v ? u : v;
   }
+  __syncthreads();  // red is reused by consecutive calls
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
   __syncthreads();
   v = red[threadIdx.x & 31];
@@ -195,36 +196,33 @@ __device__ void build_few(const PlanArgs& a, int ql, int kv, int q0, int lo,
 }
 
 // Orders the streams with rows by falling length: thread i gets the i-th's
-// number (of n_act; any number past them).
-__device__ __forceinline__ int sorted_stream(int n_streams, bool on, int nb,
-                                             int* mem) {
-  const int r = threadIdx.x;
-  // Keys hold the length (capped, which only changes the order) over the
-  // place; a bitonic network of shuffles and, across warps, shared memory.
-  uint32_t key = on ? (static_cast<uint32_t>(min(nb, (1 << 22) - 1)) << 10) |
-                          static_cast<uint32_t>(kMaxStreams - 1 - r)
-                    : 0u;
-  uint32_t* s_key = reinterpret_cast<uint32_t*>(mem);
-  int top = 32;  // the network's size
-  while (top < n_streams) top <<= 1;
-  for (int k = 2; k <= top; k <<= 1) {
-    for (int j = k >> 1; j > 0; j >>= 1) {
-      if (j >= 32) {
-        __syncthreads();
-        s_key[r] = key;
-        __syncthreads();
-      }
-      if (r < top) {  // (whole warps)
-        const uint32_t other =
-            j >= 32 ? s_key[r ^ j] : __shfl_xor_sync(0xffffffffu, key, j);
-        // falling order where bit k of r is clear (for the last k: in all
-        // places)
-        const bool keep_max = ((r & k) == 0) == ((r & j) == 0);
-        key = keep_max ? max(key, other) : min(key, other);
-      }
-    }
-  }
-  return kMaxStreams - 1 - static_cast<int>(key & (kMaxStreams - 1));
+// number (of the n_act there are; any number past them).  By length classes,
+// four to the doubling and 32 of them down from the longest, streams in
+// their own order within a class: that is close enough for CTAs that take
+// units up and down the list (a full sort of 1,024 took 6 us instead of 1).
+__device__ __forceinline__ int sorted_stream(bool on, int nb, int* order,
+                                             int* hist, uint64_t* red) {
+  const int r = threadIdx.x, lane = r & 31, warp = r >> 5;
+  const int longest =
+      static_cast<int>(block_max(static_cast<uint64_t>(on ? nb : 0), red));
+  hist[r] = 0;
+  __syncthreads();
+  int cls = 32;  // no rows
+  if (on)
+    cls = min(31, static_cast<int>(4.f * __log2f(static_cast<float>(longest) /
+                                                 static_cast<float>(nb))));
+  const unsigned same = __match_any_sync(0xffffffffu, cls);
+  const int before = __popc(same & ((1u << lane) - 1u));
+  if (on && before == 0) hist[cls * 32 + warp] = __popc(same);
+  __syncthreads();
+  const int n = hist[r];
+  const int upto = static_cast<int>(block_scan(static_cast<uint64_t>(n), red));
+  __syncthreads();
+  hist[r] = upto - n;
+  __syncthreads();
+  if (on) order[hist[cls * 32 + warp] + before] = r;
+  __syncthreads();
+  return order[r];
 }
 
 // Weights of a stream's units: nb key blocks, ql rows.
@@ -251,8 +249,11 @@ __device__ void build_tiles(const PlanArgs& a, int ql, int nb, uint64_t* red,
   __shared__ int s_units, s_act, s_long;
   __shared__ unsigned long long s_sum;
   unsigned long long* s_load = mem.load;
-  const int src =
-      a.c.n_streams > 1 ? sorted_stream(a.c.n_streams, on, nb, mem.a) : 0;
+  int src = 0;
+  if (a.c.n_streams > 1) {
+    mem.a[r] = 0;  // places past the last
+    src = sorted_stream(on, nb, mem.a, mem.b, red);
+  }
   const int n_act = __syncthreads_count(on);
   mem.a[r] = nb;
   mem.b[r] = ql;
@@ -261,7 +262,8 @@ __device__ void build_tiles(const PlanArgs& a, int ql, int nb, uint64_t* red,
   const int m_nb = mine ? mem.a[src] : 0;
   const int m_ql = mine ? mem.b[src] : 0;
   const int m_tiles = (m_ql + kTileRows - 1) / kTileRows;
-  // (lengths past 65,535 blocks are scaled so that the line fits 32 bits)
+  // (lengths past 65,535 blocks are scaled so that the line fits 32 bits; the
+  // first stream is within a fifth of the longest)
   if (r == 0) s_long = m_nb;
   __syncthreads();
   const int down = max(0, 16 - __clz(s_long));

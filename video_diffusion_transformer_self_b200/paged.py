@@ -227,7 +227,7 @@ class PagedCache:
                                           device=self.device)
         return self._workspace
 
-    def attn(self, q, k_pages, v_pages, o, softmax_scale=_SCALE, stream=None,
+    def attn(self, q, k_pages, v_pages, o, softmax_scale=None, stream=None,
              workspace=None):
         """o = softmax(q K^T scale) V over the pages for the planned rows
         (wan_paged_attn)."""
@@ -238,6 +238,8 @@ class PagedCache:
         if self._planned != self.max_new:
             # the plan divided the work for the kernel max_new picks
             raise ValueError("attn needs a plan made with the same max_new")
+        if softmax_scale is None:
+            softmax_scale = _SCALE
         if workspace is None:
             workspace = self.workspace()
         else:
