@@ -185,16 +185,48 @@ struct Segment {
   bool whole;                    // the item in full
 };
 
-// The part of an item that starts at x, up to x1 on the line.
-__device__ __forceinline__ Segment segment_at(const PagedArgs& a, int active,
-                                              int x, int x1) {
+// The work list as a warp holds it: lane i has entry i of up to 32, read
+// together with the header; longer lists are searched in memory.
+struct List {
+  int4 e0, e1;
+  int active;
+};
+
+__device__ __forceinline__ List read_list(const PagedArgs& a) {
+  List t;
+  const int lane = threadIdx.x & 31;
+  const int4* e = reinterpret_cast<const int4*>(a.c.work + pg::kHdr) +
+                  2 * min(lane, a.c.n_streams - 1);
+  t.e0 = __ldg(e);
+  t.e1 = __ldg(e + 1);
+  return t;
+}
+
+// The part of an item that starts at x, up to x1 on the line.  By the whole
+// warp, with the same x.
+__device__ __forceinline__ Segment segment_at(const PagedArgs& a,
+                                              const List& t, int x, int x1) {
+  const unsigned all = 0xffffffffu;
+  const int kvh = a.c.kv_heads;
+  const int lane = threadIdx.x & 31;
+  int4 e0, e1;
+  if (t.active <= 32) {
+    const int i =
+        31 - __clz(__ballot_sync(all, lane < t.active && t.e0.y * kvh <= x));
+    e0 = make_int4(__shfl_sync(all, t.e0.x, i), __shfl_sync(all, t.e0.y, i),
+                   __shfl_sync(all, t.e0.z, i), __shfl_sync(all, t.e0.w, i));
+    e1 = make_int4(__shfl_sync(all, t.e1.x, i), __shfl_sync(all, t.e1.y, i),
+                   __shfl_sync(all, t.e1.z, i), 0);
+  } else {
+    const int4* e = reinterpret_cast<const int4*>(
+        find_entry(a.c.work, t.active, pg::E_BASE, kvh, x));
+    e0 = __ldg(e);
+    e1 = __ldg(e + 1);
+  }
   Segment s;
-  const int4* e = reinterpret_cast<const int4*>(
-      find_entry(a.c.work, active, pg::E_BASE, a.c.kv_heads, x));
-  const int4 e0 = __ldg(e), e1 = __ldg(e + 1);
   s.stream = e0.x;
   const int n = e0.z;
-  const int local = x - e0.y * a.c.kv_heads;
+  const int local = x - e0.y * kvh;
   s.head = local / n;
   const int at = local - s.head * n;
   s.n = min(n - at, x1 - x);
@@ -259,11 +291,12 @@ __global__ void __launch_bounds__(kThreads, pg::kFewCtasPerSm)
                      const __grid_constant__ PagedArgs args) {
   extern __shared__ __align__(128) uint8_t smem_raw[];
   const int32_t* work = args.c.work;
+  List list = read_list(args);
   // {H_MODE, H_ACTIVE, H_TOTAL, H_CTAS}
   const int4 hdr = __ldg(reinterpret_cast<const int4*>(work));
   const int cta = blockIdx.x;
   if (hdr.x != pg::kModeFew || hdr.y < 1 || cta >= hdr.w) return;
-  const int active = hdr.y;
+  list.active = hdr.y;
   const pg::Line line(hdr.z, hdr.w);
   const int x0 = line.first(cta), x1 = line.first(cta + 1);
   launch_dependents();
@@ -278,7 +311,7 @@ __global__ void __launch_bounds__(kThreads, pg::kFewCtasPerSm)
   const int64_t page_bytes = head_bytes * args.c.kv_heads;
 
   // The loading side: stage lj of segment ls is the next one to fetch.
-  Segment ls = segment_at(args, active, x0, x1);
+  Segment ls = segment_at(args, list, x0, x1);
   int lx = x0;
   int lj = 0, lg = 0;
   // pages of this warp's part of the segment's stages, 32 at a time (one a
@@ -319,7 +352,7 @@ __global__ void __launch_bounds__(kThreads, pg::kFewCtasPerSm)
         lx += ls.n;
         lj = 0;
         if (lx < x1) {
-          ls = segment_at(args, active, lx, x1);
+          ls = segment_at(args, list, lx, x1);
           pages = pages_from(0);
         }
       } else if ((lj & 31) == 0) {
@@ -562,7 +595,7 @@ __global__ void __launch_bounds__(kThreads, pg::kFewCtasPerSm)
     }
     x += s.n;
     if (x >= x1) break;
-    s = segment_at(args, active, x, x1);
+    s = segment_at(args, list, x, x1);
     load_rows(s);
   }
 }
