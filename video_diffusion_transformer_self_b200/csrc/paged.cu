@@ -57,7 +57,14 @@ namespace {
 // old state and the pages coming back from the writes of the new state and
 // the pages going out, so no second launch is needed and no CTA waits for
 // another kernel.
+// Threads of a CTA, T below: at least one a stream and one an SM.  Every warp
+// runs the scans, so up to 64 streams take 256 threads (4,685 records of one
+// stream: 7.1 us against 9.8 with 1,024; 32 streams, 23,243 records: 12.1 and
+// 13.4; 100 streams: 16.2 and 16.1; 256: 11.4 and 10.5), more streams or
+// records 1,024.
 constexpr int kPlanThreads = 1024;
+constexpr int kPlanThreadsFew = 256;
+constexpr int kPlanStreamsFew = 64;
 
 struct PlanArgs {
   wan_paged_t c;
@@ -89,6 +96,7 @@ __device__ __forceinline__ void cluster_wait() {
 
 // Inclusive sum over the block's threads.  one_warp: only the first 32
 // threads have values (up to 32 streams): one level of the two.
+template <int T>
 __device__ __forceinline__ uint64_t block_scan(uint64_t v, uint64_t* red,
                                                bool one_warp = false) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -102,18 +110,19 @@ __device__ __forceinline__ uint64_t block_scan(uint64_t v, uint64_t* red,
   __syncthreads();
   if (one_warp) return warp ? red[0] : v;
   if (warp == 0) {
-    uint64_t t = red[lane];
+    uint64_t t = lane < T / 32 ? red[lane] : 0;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const uint64_t u = __shfl_up_sync(0xffffffffu, t, o);
       if (lane >= o) t += u;
     }
-    red[lane] = t;
+    if (lane < T / 32) red[lane] = t;
   }
   __syncthreads();
   return warp ? v + red[warp - 1] : v;
 }
 
+template <int T>
 __device__ __forceinline__ uint64_t block_max(uint64_t v, uint64_t* red) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
@@ -123,7 +132,7 @@ __device__ __forceinline__ uint64_t block_max(uint64_t v, uint64_t* red) {
   __syncthreads();  // red is reused by consecutive calls
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
   __syncthreads();
-  v = red[threadIdx.x & 31];
+  v = red[threadIdx.x & (T / 32 - 1)];
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     const uint64_t u = __shfl_xor_sync(0xffffffffu, v, o);
@@ -159,6 +168,7 @@ struct WorkMem {
 // The few-row kernel's line: 64-key stages from the first row's first key to
 // the end of the stream; at least one, so that rows that see nothing are
 // written too.
+template <int T>
 __device__ void build_few(const PlanArgs& a, int ql, int kv, int q0, int lo,
                           uint64_t* red) {
   const int r = threadIdx.x;
@@ -166,7 +176,7 @@ __device__ void build_few(const PlanArgs& a, int ql, int kv, int q0, int lo,
   const bool on = ql > 0;
   const int stage0 = on ? min(lo, kv - 1) / kStage : 0;
   const int n = on ? (kv + kStage - 1) / kStage - stage0 : 0;
-  const uint64_t sc = block_scan(
+  const uint64_t sc = block_scan<T>(
       (static_cast<uint64_t>(on) << 40) | static_cast<uint64_t>(n), red,
       a.c.n_streams <= 32);
   const int idx = static_cast<int>(sc >> 40) - on;
@@ -181,7 +191,7 @@ __device__ void build_few(const PlanArgs& a, int ql, int kv, int q0, int lo,
     e[E_ROWS] = ql;
     e[E_Q0] = q0;
   }
-  if (r == blockDim.x - 1) {
+  if (r == T - 1) {
     const int64_t total = static_cast<int64_t>(base + n) * a.c.kv_heads;
     // a stage each up to one CTA an SM, then two (12 heads over 2,000 keys,
     // 384 stages: 8.3 us on 192 CTAs, 9.0 on 296)
@@ -200,11 +210,12 @@ __device__ void build_few(const PlanArgs& a, int ql, int kv, int q0, int lo,
 // four to the doubling and 32 of them down from the longest, streams in
 // their own order within a class: that is close enough for CTAs that take
 // units up and down the list (a full sort of 1,024 took 6 us instead of 1).
+template <int T>
 __device__ __forceinline__ int sorted_stream(bool on, int nb, int* order,
                                              int* hist, uint64_t* red) {
   const int r = threadIdx.x, lane = r & 31, warp = r >> 5;
   const int longest =
-      static_cast<int>(block_max(static_cast<uint64_t>(on ? nb : 0), red));
+      static_cast<int>(block_max<T>(static_cast<uint64_t>(on ? nb : 0), red));
   hist[r] = 0;
   __syncthreads();
   int cls = 32;  // no rows
@@ -213,14 +224,14 @@ __device__ __forceinline__ int sorted_stream(bool on, int nb, int* order,
                                                  static_cast<float>(nb))));
   const unsigned same = __match_any_sync(0xffffffffu, cls);
   const int before = __popc(same & ((1u << lane) - 1u));
-  if (on && before == 0) hist[cls * 32 + warp] = __popc(same);
+  if (on && before == 0) hist[cls * (T / 32) + warp] = __popc(same);
   __syncthreads();
   const int n = hist[r];
-  const int upto = static_cast<int>(block_scan(static_cast<uint64_t>(n), red));
+  const int upto = static_cast<int>(block_scan<T>(static_cast<uint64_t>(n), red));
   __syncthreads();
   hist[r] = upto - n;
   __syncthreads();
-  if (on) order[hist[cls * 32 + warp] + before] = r;
+  if (on) order[hist[cls * (T / 32) + warp] + before] = r;
   __syncthreads();
   return order[r];
 }
@@ -240,6 +251,7 @@ __device__ __forceinline__ int last_weight(int nb, int ql) {
 // blocks are read once into L2); a last round that is not full would leave
 // SMs idle (760 units on 148 SMs are 5.14 rounds: 14 % of the time), so the
 // last one to two rounds' units are cut by weight instead.
+template <int T>
 __device__ void build_tiles(const PlanArgs& a, int ql, int nb, uint64_t* red,
                             const WorkMem& mem) {
   const int r = threadIdx.x;
@@ -252,7 +264,7 @@ __device__ void build_tiles(const PlanArgs& a, int ql, int nb, uint64_t* red,
   int src = 0;
   if (a.c.n_streams > 1) {
     mem.a[r] = 0;  // places past the last
-    src = sorted_stream(on, nb, mem.a, mem.b, red);
+    src = sorted_stream<T>(on, nb, mem.a, mem.b, red);
   }
   const int n_act = __syncthreads_count(on);
   mem.a[r] = nb;
@@ -271,18 +283,18 @@ __device__ void build_tiles(const PlanArgs& a, int ql, int nb, uint64_t* red,
   const int m_full = full_weight(w_nb), m_last = last_weight(w_nb, m_ql);
   const int units = m_tiles * heads;
   const int upto =
-      static_cast<int>(block_scan(static_cast<uint64_t>(units), red, small));
+      static_cast<int>(block_scan<T>(static_cast<uint64_t>(units), red, small));
   const uint64_t weight =
       mine ? static_cast<uint64_t>(heads) *
                  (static_cast<uint64_t>(m_tiles - 1) * m_full + m_last)
            : 0;
-  const uint64_t all = block_scan(weight, red, small);
+  const uint64_t all = block_scan<T>(weight, red, small);
   __syncthreads();
   mem.a[r] = upto;           // units up to and with the r-th stream
   mem.b[r] = m_tiles;
   mem.c[r] = m_full;
   mem.d[r] = m_last;
-  if (r == kPlanThreads - 1) {
+  if (r == T - 1) {
     s_units = upto;
     s_act = n_act;
     s_sum = all;
@@ -303,7 +315,7 @@ __device__ void build_tiles(const PlanArgs& a, int ql, int nb, uint64_t* red,
   int K = U / G;
   uint64_t lack = 1;
   if (K < kManyRounds) {
-    const int share = kPlanThreads / G;
+    const int share = T / G;
     const int c = r % G, part = r / G;
     auto unit_weight = [&](int u) {
       const int i = find_stream(mem.a, n_act, u);
@@ -320,7 +332,7 @@ __device__ void build_tiles(const PlanArgs& a, int ql, int nb, uint64_t* red,
     }
     for (int tries = 0;; ++tries) {
       __syncthreads();
-      const uint64_t top = block_max(r < G ? s_load[r] : 0, red);
+      const uint64_t top = block_max<T>(r < G ? s_load[r] : 0, red);
       if (K == 0 || tries == 2 || top * G <= s_sum) break;
       --K;
       if (r < G) s_load[r] -= unit_weight(K * G + (K & 1 ? G - 1 - r : r));
@@ -330,7 +342,7 @@ __device__ void build_tiles(const PlanArgs& a, int ql, int nb, uint64_t* red,
     lack = r < G && s_load[r] < mean ? mean - s_load[r] : 0;
   }
   // the line: places in proportion to what each CTA lacks
-  const uint64_t lack_upto = block_scan(r < G ? lack : 0, red);
+  const uint64_t lack_upto = block_scan<T>(r < G ? lack : 0, red);
   const int first = K * G;  // units before the line
   const int base = upto - units;
   // the stream's units before the line
@@ -338,9 +350,9 @@ __device__ void build_tiles(const PlanArgs& a, int ql, int nb, uint64_t* red,
   const uint64_t skipped =
       mine ? weight_before(before, m_tiles, m_full, m_last) : 0;
   const uint64_t on_line = weight - skipped;
-  const uint64_t line_upto = block_scan(on_line, red, small);
+  const uint64_t line_upto = block_scan<T>(on_line, red, small);
   __shared__ unsigned long long s_lack, s_line;
-  if (r == kPlanThreads - 1) {
+  if (r == T - 1) {
     s_lack = lack_upto;
     s_line = line_upto;
   }
@@ -377,7 +389,7 @@ __device__ void build_tiles(const PlanArgs& a, int ql, int nb, uint64_t* red,
   }
   __syncthreads();
   // what the joining pass needs of every unit on the line
-  for (int j = r; j < U - first; j += kPlanThreads) {
+  for (int j = r; j < U - first; j += T) {
     const int u = first + j;
     const int i = find_stream(mem.a, n_act, u);
     const int local = u - (i ? mem.a[i - 1] : 0);
@@ -412,22 +424,24 @@ __device__ void build_tiles(const PlanArgs& a, int ql, int nb, uint64_t* red,
 
 // The attention's work list, by one CTA.  ql and kv are stream threadIdx.x's
 // rows and keys, q0 its first packed row.
+template <int T>
 __device__ void build_work(const PlanArgs& a, int ql, int kv, int q0,
                            int chunk, int window, uint64_t* red,
                            const WorkMem& mem) {
   const int lo = ql > 0 ? key_lo(kv - ql, chunk, window) : 0;
   if (a.few) {
-    build_few(a, ql, kv, q0, lo, red);
+    build_few<T>(a, ql, kv, q0, lo, red);
     return;
   }
   // 128-key blocks of the longest tile (an upper bound under a window)
   int nb = 0;
   if (ql > 0)
     nb = max((kv + kBlock - 1) / kBlock - min(lo, kv - 1) / kBlock, 1);
-  build_tiles(a, ql, nb, red, mem);
+  build_tiles<T>(a, ql, nb, red, mem);
 }
 
-__global__ void __launch_bounds__(kPlanThreads)
+template <int T>
+__global__ void __launch_bounds__(T)
     paged_plan_kernel(const __grid_constant__ PlanArgs a) {
   __shared__ uint64_t red[32];
   __shared__ int s_end[kMaxStreams];    // packed rows up to and with stream r
@@ -461,7 +475,7 @@ __global__ void __launch_bounds__(kPlanThreads)
   const int rows = max(nw, 0);
   const bool ended = nw < 0;
   const int64_t end =
-      static_cast<int64_t>(block_scan(static_cast<uint64_t>(rows), red, R <= 32));
+      static_cast<int64_t>(block_scan<T>(static_cast<uint64_t>(rows), red, R <= 32));
   const int64_t total = static_cast<int64_t>(old) + rows;
   const int64_t cap = c.token_cap;
   const bool fit =
@@ -484,7 +498,7 @@ __global__ void __launch_bounds__(kPlanThreads)
   const int top =
       valid ? static_cast<int>((total + ps - 1) >> a.page_shift) : held;
   const int need = valid ? top - held : 0;
-  const uint64_t sums = block_scan(
+  const uint64_t sums = block_scan<T>(
       (static_cast<uint64_t>(back) << 32) | static_cast<uint64_t>(need), red,
       R <= 32);
   const int back_incl = static_cast<int>(sums >> 32);
@@ -494,7 +508,7 @@ __global__ void __launch_bounds__(kPlanThreads)
   s_old[r] = old;
   s_end[r] = static_cast<int>(end < cap ? end : cap);
   __syncthreads();
-  const int n_back = s_back[kMaxStreams - 1];
+  const int n_back = s_back[T - 1];
   const int free_now = min(count + n_back, c.n_pages);
   const bool admit = valid && need_incl <= free_now;
   s_need[r] = need_incl;
@@ -508,9 +522,9 @@ __global__ void __launch_bounds__(kPlanThreads)
   // admission stops for good at the first stream that does not fit, so the
   // admitted needs are a prefix of the line of needs
   const int n_out = static_cast<int>(
-      block_scan(admit ? static_cast<uint64_t>(need) : 0ull, red, R <= 32));
+      block_scan<T>(admit ? static_cast<uint64_t>(need) : 0ull, red, R <= 32));
   __shared__ int s_out;
-  if (r == kPlanThreads - 1) s_out = n_out;
+  if (r == T - 1) s_out = n_out;
   const WorkMem mem = {s_back,
                        s_need,
                        s_from,
@@ -526,8 +540,8 @@ __global__ void __launch_bounds__(kPlanThreads)
   // with a cluster its last CTA divides the attention's work (no global
   // state but its own output) and the others do the moves
   const int movers = ctas > 1 ? ctas - 1 : 1;
-  const int step = movers * kPlanThreads;
-  const int me = rank * kPlanThreads + r;
+  const int step = movers * T;
+  const int me = rank * T + r;
   if (rank < movers) {
     for (int i = me; i < n_back; i += step) {
       const int q = find_stream(s_back, R, i);
@@ -541,7 +555,7 @@ __global__ void __launch_bounds__(kPlanThreads)
   __syncthreads();
   if (ctas > 1) cluster_arrive();
   if (rank == movers) {
-    build_work(a, admit ? rows : 0, kv, r ? s_end[r - 1] : 0, cfg.z, cfg.w,
+    build_work<T>(a, admit ? rows : 0, kv, r ? s_end[r - 1] : 0, cfg.z, cfg.w,
                red, mem);
     __syncthreads();
     cluster_wait();
@@ -580,31 +594,47 @@ __global__ void __launch_bounds__(kPlanThreads)
   // between them; divisions by a stream's frame and row are products.
   int4* tok = reinterpret_cast<int4*>(c.tokens);
   const int n_rows = s_end[R - 1];
-  const int warps = movers * (kPlanThreads / 32);
+  const int warps = movers * (T / 32);
   const int share = ((c.token_cap + warps - 1) / warps + 31) & ~31;
   const int i0 = (me >> 5) * share;
   const int i1 = min(i0 + share, c.token_cap);
   int q = i0 < n_rows ? find_stream(s_end, R, min(i0 + (r & 31), n_rows - 1))
                       : 0;
+  // the stream's numbers stay in registers while it lasts
+  int upto = -1, start = 0, live = 0, old_q = 0, hw = 1, w = 1, held_q = 0;
+  float inv_hw = 1.f, inv_w = 1.f;
+  uint32_t from = 0;  // ring place of its first new page
   for (int i = i0 + (r & 31); i < i1; i += 32) {
     int4 rec = make_int4(0, 0, 0, -1);
     if (i < n_rows) {
-      while (s_end[q] <= i) ++q;
-      // rows of the stream start where those of the one before end
-      const int off = i - (q ? s_end[q - 1] : 0);
-      if (off < s_rows[q]) {
-        const int pos = s_old[q] + off;
-        rec.x = div_by(pos, s_hw[q], s_inv_hw[q]);
-        const int rest = pos - rec.x * s_hw[q];
-        rec.y = div_by(rest, s_w[q], s_inv_w[q]);
-        rec.z = rest - rec.y * s_w[q];
+      if (i >= upto) {
+        while (s_end[q] <= i) ++q;
+        upto = s_end[q];
+        // rows of the stream start where those of the one before end
+        start = q ? s_end[q - 1] : 0;
+        live = s_rows[q];
+        old_q = s_old[q];
+        hw = s_hw[q];
+        w = s_w[q];
+        inv_hw = s_inv_hw[q];
+        inv_w = s_inv_w[q];
+        held_q = (old_q + ps - 1) >> a.page_shift;
+        from = head + (q ? s_need[q - 1] : 0);
+      }
+      const int off = i - start;
+      if (off < live) {
+        const int pos = old_q + off;
+        rec.x = div_by(pos, hw, inv_hw);
+        const int rest = pos - rec.x * hw;
+        rec.y = div_by(rest, w, inv_w);
+        rec.z = rest - rec.y * w;
         const int p = pos >> a.page_shift;
-        const int h0 = (s_old[q] + ps - 1) >> a.page_shift;
-        int page;
-        if (p < h0)
-          page = c.block_table[static_cast<int64_t>(q) * c.max_pages + p];
-        else
-          page = c.free_ring[(head + (q ? s_need[q - 1] : 0) + (p - h0)) % np];
+        // (the ring's place is below 2 np: what goes out is at most np)
+        const uint32_t at = from + (p - held_q);
+        const int page =
+            p < held_q
+                ? c.block_table[static_cast<int64_t>(q) * c.max_pages + p]
+                : c.free_ring[at < np ? at : at - np];
         rec.w = (page << a.page_shift) + (pos & (ps - 1));
       }
     }
@@ -612,7 +642,7 @@ __global__ void __launch_bounds__(kPlanThreads)
   }
   if (ctas == 1) {
     __syncthreads();
-    build_work(a, admit ? rows : 0, kv, r ? s_end[r - 1] : 0, cfg.z, cfg.w,
+    build_work<T>(a, admit ? rows : 0, kv, r ? s_end[r - 1] : 0, cfg.z, cfg.w,
                red, mem);
   }
 }
@@ -772,7 +802,7 @@ unsigned big_cluster(int dev) {
   std::lock_guard<std::mutex> lock(mu);
   if (size[dev] == 0) {
     size[dev] = 8;
-    if (cudaFuncSetAttribute(paged_plan_kernel,
+    if (cudaFuncSetAttribute(paged_plan_kernel<kPlanThreads>,
                              cudaFuncAttributeNonPortableClusterSizeAllowed,
                              1) == cudaSuccess) {
       cudaLaunchConfig_t cfg = {};
@@ -786,7 +816,7 @@ unsigned big_cluster(int dev) {
       cfg.attrs = at;
       cfg.numAttrs = 1;
       int n = 0;
-      if (cudaOccupancyMaxActiveClusters(&n, paged_plan_kernel, &cfg) ==
+      if (cudaOccupancyMaxActiveClusters(&n, paged_plan_kernel<kPlanThreads>, &cfg) ==
               cudaSuccess &&
           n > 0)
         size[dev] = 16;
@@ -832,15 +862,17 @@ int wan_paged_plan(const wan_paged_t* c, const int32_t* new_lens, void* s) {
   if (a.sms < 1 || a.sms * kFewCtasPerSm > kMaxCtas) return WAN_ECUDA;
   a.few = few_mode(c) ? 1 : 0;
   cudaLaunchConfig_t cfg = {};
-  // One CTA up to 2,048 records (two a thread), a cluster of 8 up to 32,768,
+  // One CTA up to 2,048 records, a cluster of 8 up to 32,768,
   // of 16 beyond where the device can run one (114,041 records of 48
-  // streams: 13.4 us with 16, 18.7 with 8; 4,685 records: 9.7 us with 8, 13.2
-  // with one CTA).
-  const unsigned ctas = c->token_cap <= 2 * kPlanThreads    ? 1
-                        : c->token_cap <= 32 * kPlanThreads ? 8
-                                                            : big_cluster(dev);
+  // streams: 13.4 us with 16, 18.7 with 8; 4,685 records, 1,024 threads: 9.7
+  // us with 8, 13.2 with one CTA).
+  const bool few = c->n_streams <= kPlanStreamsFew &&
+                   a.sms <= kPlanThreadsFew && c->token_cap <= 32768;
+  const unsigned ctas = c->token_cap <= 2048    ? 1
+                        : c->token_cap <= 32768 ? 8
+                                                : big_cluster(dev);
   cfg.gridDim = dim3(ctas);
-  cfg.blockDim = dim3(kPlanThreads);
+  cfg.blockDim = dim3(few ? kPlanThreadsFew : kPlanThreads);
   cfg.stream = as_stream(s);
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
@@ -849,7 +881,10 @@ int wan_paged_plan(const wan_paged_t* c, const int32_t* new_lens, void* s) {
   at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, paged_plan_kernel, a) == cudaSuccess
+  return cudaLaunchKernelEx(&cfg,
+                            few ? paged_plan_kernel<kPlanThreadsFew>
+                                : paged_plan_kernel<kPlanThreads>,
+                            a) == cudaSuccess
              ? WAN_OK
              : WAN_ECUDA;
 }
