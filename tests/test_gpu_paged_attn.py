@@ -402,3 +402,16 @@ def test_pools_past_32_bit_offsets(max_new):
     ref = np.einsum("hij,jhd->ihd", p, f64(vals))
     mag = np.einsum("hij,jhd->ihd", p, np.abs(f64(vals)))
     assert_attn(f64(o)[:7], ref, mag, "large pool", 40.0)
+
+
+@pytest.mark.parametrize("R,max_new", [(33, 2), (100, 1), (1024, 3),
+                                       (70, 130)])
+def test_many_streams(R, max_new):
+    # work lists past one warp's width: searched in memory
+    rng = np.random.default_rng(R)
+    streams = [(2, 3, int(rng.choice([1, 6])), int(rng.choice([0, 12])))
+               for _ in range(R)]
+    steps = [[int(x) for x in rng.integers(0, max_new + 1, R)]
+             for _ in range(4)]
+    _run(streams, (200, 2, 3), 16, 2, 1, steps, 77 + R, max_new,
+         R * (1 + 4 * max_new // 16) + R + 20, check=(0, 3))
