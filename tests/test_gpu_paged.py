@@ -165,7 +165,8 @@ def _write_case(heads, kv_heads, ps, streams, grid, steps, spare, seed,
 # heads across the register variants (4, 6, 8, 12, 20 rows a lane) and the
 # two-pass one, shared key heads, odd counts
 @pytest.mark.parametrize("heads,kv_heads", [
-    (1, 1), (2, 2), (7, 7), (8, 2), (9, 3), (12, 12), (13, 1), (16, 1), (17, 17),
+    (1, 1), (2, 2), (7, 7), (8, 2), (9, 3), (12, 12), (13, 1), (16, 1),
+    (17, 17),
     (25, 5), (40, 40), (40, 8), (41, 41), (48, 6)])
 def test_write_heads(heads, kv_heads):
     _write_case(heads, kv_heads, 32, [(3, 4, 12, 0), (2, 5, 10, 0)],

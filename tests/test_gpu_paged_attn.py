@@ -131,8 +131,9 @@ def test_tiles_ragged_streams(ps, heads, kv_heads):
           [40, 513, -1, 1, 2, 5, 0]), 500 + ps, 600, 260)
 
 
-@pytest.mark.parametrize("window,chunk", [(0, 1), (0, 20), (40, 20), (7, 20),
-                                          (300, 60), (130, 1), (0, 2 ** 31 - 1)])
+@pytest.mark.parametrize("window,chunk", [
+    (0, 1), (0, 20), (40, 20), (7, 20), (300, 60), (130, 1),
+    (0, 2 ** 31 - 1)])
 def test_tiles_windows_and_chunks(window, chunk):
     streams = [(4, 5, chunk, window), (5, 5, chunk, window)]
     _run(streams, (80, 5, 5), 16, 2, 2,
