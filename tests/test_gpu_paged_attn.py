@@ -416,3 +416,16 @@ def test_many_streams(R, max_new):
              for _ in range(4)]
     _run(streams, (200, 2, 3), 16, 2, 1, steps, 77 + R, max_new,
          R * (1 + 4 * max_new // 16) + R + 20, check=(0, 3))
+
+
+# head groups of a row tile: all heads of one key head, a divisor of them, one
+# (a prime past 16), and long streams whose tiles would not come out even
+@pytest.mark.parametrize("heads,kv_heads,max_new", [
+    (5, 1, 300), (16, 1, 300), (20, 1, 200), (17, 1, 100), (32, 1, 100),
+    (14, 2, 300), (5, 1, 1100), (8, 2, 1100)])
+def test_tiles_head_groups(heads, kv_heads, max_new):
+    streams = [(4, 5, 20, 0), (4, 5, 7, 50), (4, 5, 1, 0)]
+    m = max_new
+    _run(streams, (130, 4, 5), 16, heads, kv_heads,
+         ([m, 1, 26], [25, m, 127], [51, 130, 3]), 60 + heads, m,
+         3 * (2 * m + 200) // 16 + 40)

@@ -75,6 +75,7 @@ struct PlanArgs {
   int page_shift;
   int sms;
   int few;
+  int pack, tile_tokens;  // of the tile kernel
 };
 
 // n / d for 0 <= n < 2^31, 1 <= d <= 2^20, inv = 1 / d rounded.  The three
@@ -157,13 +158,16 @@ __device__ __forceinline__ int find_stream(const int* incl, int n, int x) {
   return lo;
 }
 
+// The least weight of a piece that a cut leaves (a piece costs its start, its
+// partial result and the join of it, about six key blocks).
+constexpr int kMinPiece = 64;
+
 // Rounds of whole units beyond which the CTAs' loads count as equal.
 constexpr int kManyRounds = 16;
 
 // Scratch of build_work, one entry a stream or CTA.
 struct WorkMem {
-  int *a, *b, *c, *d, *e, *f;
-  const int* end;             // packed rows up to and with each stream
+  int *a, *b, *c, *d, *e, *f, *g;
   unsigned long long* load;   // one a CTA
   int64_t* start;             // one a stream
 };
@@ -210,13 +214,15 @@ __device__ void build_few(const PlanArgs& a, int ql, int kv, int q0, int lo,
 }
 
 // Orders the streams with rows by falling length: thread i gets the i-th's
-// number (of the n_act there are; any number past them).  By length classes,
+// number (of the n_act there are; any number past them), and stream i's place
+// in *place.  By length classes,
 // four to the doubling and 32 of them down from the longest, streams in
 // their own order within a class: that is close enough for CTAs that take
 // units up and down the list (a full sort of 1,024 took 6 us instead of 1).
 template <int T>
 __device__ __forceinline__ int sorted_stream(bool on, int nb, int* order,
-                                             int* hist, uint64_t* red) {
+                                             int* hist, uint64_t* red,
+                                             int* place) {
   const int r = threadIdx.x, lane = r & 31, warp = r >> 5;
   const int longest =
       static_cast<int>(block_max<T>(static_cast<uint64_t>(on ? nb : 0), red));
@@ -236,18 +242,21 @@ __device__ __forceinline__ int sorted_stream(bool on, int nb, int* order,
   __syncthreads();
   hist[r] = upto - n;
   __syncthreads();
-  if (on) order[hist[cls * (T / 32) + warp] + before] = r;
+  if (on) {
+    *place = hist[cls * (T / 32) + warp] + before;
+    order[*place] = r;
+  }
   __syncthreads();
   return order[r];
 }
 
-// Weights of a stream's units: nb key blocks, ql rows.
+// Weights of a stream's units: nb key blocks, ql new tokens, `tokens` a tile.
 __device__ __forceinline__ int full_weight(int nb) {
   return kPairWeight * nb + kUnitWeight;
 }
-__device__ __forceinline__ int last_weight(int nb, int ql) {
-  const int rest = ql & (kTileRows - 1);
-  return (rest >= 1 && rest <= kBlock ? kOneWeight : kPairWeight) * nb +
+__device__ __forceinline__ int last_weight(int nb, int ql, int tokens) {
+  const int rest = ql % (2 * tokens);
+  return (rest >= 1 && rest <= tokens ? kOneWeight : kPairWeight) * nb +
          kUnitWeight;
 }
 
@@ -257,19 +266,21 @@ __device__ __forceinline__ int last_weight(int nb, int ql) {
 // SMs idle (760 units on 148 SMs are 5.14 rounds: 14 % of the time), so the
 // last one to two rounds' units are cut by weight instead.
 template <int T>
-__device__ void build_tiles(const PlanArgs& a, int ql, int nb, uint64_t* red,
+__device__ void build_tiles(const PlanArgs& a, int ql, int kv, int q0,
+                            int chunk, int window, int nb, uint64_t* red,
                             const WorkMem& mem) {
   const int r = threadIdx.x;
   const bool on = ql > 0;
   const bool small = a.c.n_streams <= 32;
-  const int heads = a.c.heads;
+  const int heads = a.c.heads / a.pack;  // head groups of a tile
+  const int pair = 2 * a.tile_tokens;
   __shared__ int s_units, s_act, s_long;
   __shared__ unsigned long long s_sum;
   unsigned long long* s_load = mem.load;
-  int src = 0;
+  int src = 0, place = 0;
   if (a.c.n_streams > 1) {
     mem.a[r] = 0;  // places past the last
-    src = sorted_stream<T>(on, nb, mem.a, mem.b, red);
+    src = sorted_stream<T>(on, nb, mem.a, mem.b, red, &place);
   }
   const int n_act = __syncthreads_count(on);
   mem.a[r] = nb;
@@ -278,14 +289,15 @@ __device__ void build_tiles(const PlanArgs& a, int ql, int nb, uint64_t* red,
   const bool mine = r < n_act;
   const int m_nb = mine ? mem.a[src] : 0;
   const int m_ql = mine ? mem.b[src] : 0;
-  const int m_tiles = (m_ql + kTileRows - 1) / kTileRows;
+  const int m_tiles = (m_ql + pair - 1) / pair;
   // (lengths past 65,535 blocks are scaled so that the line fits 32 bits; the
   // first stream is within a fifth of the longest)
   if (r == 0) s_long = m_nb;
   __syncthreads();
   const int down = max(0, 16 - __clz(s_long));
   const int w_nb = m_nb >> down;
-  const int m_full = full_weight(w_nb), m_last = last_weight(w_nb, m_ql);
+  const int m_full = full_weight(w_nb);
+  const int m_last = last_weight(w_nb, m_ql, a.tile_tokens);
   const int units = m_tiles * heads;
   const int upto =
       static_cast<int>(block_scan<T>(static_cast<uint64_t>(units), red, small));
@@ -365,16 +377,15 @@ __device__ void build_tiles(const PlanArgs& a, int ql, int nb, uint64_t* red,
   int32_t* work = a.c.work;
   int* s_cut = reinterpret_cast<int*>(s_load);
   __syncthreads();
-  if (r < G) {
-    // (fp32: a cut may be off by a few places, but cuts do not cross)
-    const float scale = static_cast<float>(s_line) /
-                        static_cast<float>(s_lack ? s_lack : 1);
-    int end = static_cast<int>(s_line);
-    if (r < G - 1)
-      end = min(end, static_cast<int>(static_cast<float>(lack_upto) * scale));
-    s_cut[r + 1] = end;
-    work[kLine + r + 1] = end;
-    if (r == 0) s_cut[0] = work[kLine] = 0;
+  if (on) {
+    // thread r has stream r here, the entries' threads their place
+    int32_t* e = work + kHdr + kEnt * place;
+    e[E_TKV] = kv;
+    e[E_TROWS] = ql;
+    e[E_TQ0] = q0;
+    e[E_CHUNK] = chunk;
+    e[E_WINDOW] = window;
+    mem.e[place] = q0;
   }
   if (mine) {
     int32_t* e = work + kHdr + kEnt * r;
@@ -387,9 +398,35 @@ __device__ void build_tiles(const PlanArgs& a, int ql, int nb, uint64_t* red,
                           static_cast<int64_t>(skipped);
     e[E_FIRST] = static_cast<int>(line_upto - on_line);
     *reinterpret_cast<int64_t*>(e + E_LINE) = start;
-    mem.e[r] = src;
     mem.f[r] = m_ql;
     mem.start[r] = start;
+    mem.g[r] = static_cast<int>(line_upto);
+  }
+  __syncthreads();
+  if (r < G) {
+    // (fp32: a cut may be off by a few places, but cuts do not cross)
+    const float scale = static_cast<float>(s_line) /
+                        static_cast<float>(s_lack ? s_lack : 1);
+    int end = static_cast<int>(s_line);
+    if (r < G - 1) {
+      end = min(end, static_cast<int>(static_cast<float>(lack_upto) * scale));
+      if (end < static_cast<int>(s_line)) {
+        // the unit it falls into, and no piece too small to pay for itself
+        const int i = find_stream(mem.g, n_act, end);
+        const int64_t y = end - mem.start[i];
+        const int full = mem.c[i], last = mem.d[i];
+        const int64_t period =
+            static_cast<int64_t>(mem.b[i] - 1) * full + last;
+        const int rest = static_cast<int>(y % period);
+        const int len = rest < last ? last : full;
+        const int off = rest < last ? rest : (rest - last) % full;
+        if (off < kMinPiece || len - off < kMinPiece)
+          end += 2 * off < len ? -off : len - off;
+      }
+    }
+    s_cut[r + 1] = end;
+    work[kLine + r + 1] = end;
+    if (r == 0) s_cut[0] = work[kLine] = 0;
   }
   __syncthreads();
   // what the joining pass needs of every unit on the line
@@ -405,11 +442,11 @@ __device__ void build_tiles(const PlanArgs& a, int ql, int nb, uint64_t* red,
     // CTAs that hold its first and its last place
     const int c0 = find_stream(s_cut + 1, G, x0);
     const int c1 = find_stream(s_cut + 1, G, x1);
-    const int row0 = (tiles - 1 - tile) * kTileRows;
+    const int tok0 = (tiles - 1 - tile) * pair;
     int32_t rec[kJoinInts] = {0, 0, 0, 0, 0, 0, 0, 0};
-    rec[J_ROW] = (mem.e[i] ? mem.end[mem.e[i] - 1] : 0) + row0;
-    rec[J_ROWS] = c0 == c1 ? 0 : min(mem.f[i] - row0, kTileRows);
-    rec[J_HEAD] = head;
+    rec[J_ROW] = mem.e[i] + tok0;
+    rec[J_TOKENS] = c0 == c1 ? 0 : min(mem.f[i] - tok0, pair);
+    rec[J_HEAD] = head * a.pack;
     rec[J_PART] = 2 * c0 + (x0 > s_cut[c0] ? 1 : 0);
     rec[J_CTA] = c0 + 1;
     rec[J_PARTS] = c1 - c0 + 1;
@@ -439,27 +476,36 @@ __device__ void build_work(const PlanArgs& a, int ql, int kv, int q0,
   }
   // 128-key blocks of the longest tile (an upper bound under a window)
   int nb = 0;
-  if (ql > 0)
+  if (ql > 0) {
     nb = max((kv + kBlock - 1) / kBlock - min(lo, kv - 1) / kBlock, 1);
-  build_tiles<T>(a, ql, nb, red, mem);
+    if (window > 0) {
+      const int64_t rows = 2 * a.tile_tokens;
+      const int64_t keys = window + (rows + chunk - 1) / chunk * chunk;
+      nb = static_cast<int>(min(static_cast<int64_t>(nb), keys / kBlock + 2));
+    }
+  }
+  build_tiles<T>(a, ql, kv, q0, chunk, window, nb, red, mem);
 }
 
 template <int T>
 __global__ void __launch_bounds__(T)
     paged_plan_kernel(const __grid_constant__ PlanArgs a) {
+  // (s_inv_w also serves as scratch: a 64-bit number a CTA)
+  constexpr int kScratch = T > 2 * (kMaxCtas + 1) ? T : 2 * (kMaxCtas + 1);
   __shared__ uint64_t red[32];
-  __shared__ int s_end[kMaxStreams];    // packed rows up to and with stream r
-  __shared__ int s_rows[kMaxStreams];   // admitted rows
-  __shared__ int s_back[kMaxStreams];   // pages coming back, inclusive
-  __shared__ int s_need[kMaxStreams];   // pages going out, inclusive
-  __shared__ int s_old[kMaxStreams];    // tokens before the step
-  __shared__ int s_from[kMaxStreams];   // first page coming back
+  __shared__ int s_end[T];    // packed rows up to and with stream r
+  __shared__ int s_rows[T];   // admitted rows
+  __shared__ int s_back[T];   // pages coming back, inclusive
+  __shared__ int s_need[T];   // pages going out, inclusive
+  __shared__ int s_old[T];    // tokens before the step
+  __shared__ int s_from[T];   // first page coming back
   // tokens of a frame and of a row, and one over them
-  __shared__ __align__(8) int s_dims[2 * kMaxStreams];
+  __shared__ __align__(8) int s_dims[2 * T];
   int* s_hw = s_dims;
-  int* s_w = s_dims + kMaxStreams;
-  __shared__ float s_inv_hw[kMaxStreams];
-  __shared__ __align__(8) float s_inv_w[kMaxStreams];
+  int* s_w = s_dims + T;
+  __shared__ float s_inv_hw[T];
+  __shared__ __align__(8) float s_inv_w[kScratch];
+  __shared__ int s_extra[T];            // scratch
   const wan_paged_t& c = a.c;
   const int R = c.n_streams;
   const int r = threadIdx.x;
@@ -533,15 +579,15 @@ __global__ void __launch_bounds__(T)
                        s_rows,
                        s_old,
                        reinterpret_cast<int*>(s_inv_hw),
-                       s_end,
+                       s_extra,
                        reinterpret_cast<unsigned long long*>(s_inv_w),
                        reinterpret_cast<int64_t*>(s_dims)};
   const int kv = ended ? 0 : old + (admit ? rows : 0);
   const int ctas = gridDim.x;
   const int rank = blockIdx.x;
-  // with a cluster its last CTA divides the attention's work (no global
-  // state but its own output) and the others do the moves
-  const int movers = ctas > 1 ? ctas - 1 : 1;
+  // the last CTA divides the attention's work (no global state but its own
+  // output), the others do the moves
+  const int movers = ctas - 1;
   const int step = movers * T;
   const int me = rank * T + r;
   if (rank < movers) {
@@ -555,7 +601,7 @@ __global__ void __launch_bounds__(T)
     }
   }
   __syncthreads();
-  if (ctas > 1) cluster_arrive();
+  cluster_arrive();
   if (rank == movers) {
     build_work<T>(a, admit ? rows : 0, kv, r ? s_end[r - 1] : 0, cfg.z, cfg.w,
                   red, mem);
@@ -564,7 +610,7 @@ __global__ void __launch_bounds__(T)
     return;
   }
   // once all pages are back and all CTAs have read the old state
-  if (ctas > 1) cluster_wait();
+  cluster_wait();
   const int out = s_out;
   for (int i = me; i < out; i += step) {
     const int q = find_stream(s_need, R, i);
@@ -641,11 +687,6 @@ __global__ void __launch_bounds__(T)
       }
     }
     tok[i] = rec;
-  }
-  if (ctas == 1) {
-    __syncthreads();
-    build_work<T>(a, admit ? rows : 0, kv, r ? s_end[r - 1] : 0, cfg.z, cfg.w,
-                  red, mem);
   }
 }
 
@@ -863,16 +904,16 @@ int wan_paged_plan(const wan_paged_t* c, const int32_t* new_lens, void* s) {
   a.sms = device_sms(dev);
   if (a.sms < 1 || a.sms * kFewCtasPerSm > kMaxCtas) return WAN_ECUDA;
   a.few = few_mode(c) ? 1 : 0;
+  a.pack = tile_pack(c);
+  a.tile_tokens = tile_tokens(c);
   cudaLaunchConfig_t cfg = {};
-  // One CTA up to 2,048 records, a cluster of 8 up to 32,768,
-  // of 16 beyond where the device can run one (114,041 records of 48
-  // streams: 13.4 us with 16, 18.7 with 8; 4,685 records, 1,024 threads: 9.7
-  // us with 8, 13.2 with one CTA).
+  // A cluster of 8 up to 32,768 records, of 16 beyond where the device can run
+  // one (114,041 records of 48 streams: 13.4 us with 16, 18.7 with 8).  One
+  // CTA is no faster for a few records (7.5 us) and takes 33 us where streams
+  // end that held thousands of pages.
   const bool few = c->n_streams <= kPlanStreamsFew &&
                    a.sms <= kPlanThreadsFew && c->token_cap <= 32768;
-  const unsigned ctas = c->token_cap <= 2048    ? 1
-                        : c->token_cap <= 32768 ? 8
-                                                : big_cluster(dev);
+  const unsigned ctas = c->token_cap <= 32768 ? 8 : big_cluster(dev);
   cfg.gridDim = dim3(ctas);
   cfg.blockDim = dim3(few ? kPlanThreadsFew : kPlanThreads);
   cfg.stream = as_stream(s);

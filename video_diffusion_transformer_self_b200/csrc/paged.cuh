@@ -18,15 +18,17 @@ constexpr int kModeNone = 0, kModeFew = 1, kModeTile = 2;
 
 // kFew: the (stream, key head, 64-key stage) items form one line that is cut
 // into equal parts, one per CTA.
-// kTile: units are (256-row tile pair, head), numbered streams by falling
-// length, then head, then tile pair (the stream's last one first: it sees the
-// most keys).  H_WAVES rounds of one whole unit per CTA come first, in turn
+// kTile: a row tile holds tile_tokens() tokens x tile_pack() query heads of
+// one key head.  Units are (tile pair, tile_pack() heads), numbered streams by
+// falling length, then heads, then tile pair (the stream's last one first: it
+// sees the most keys).  H_WAVES rounds of one whole unit per CTA come first, in turn
 // up and down the CTAs; the units behind them form a line of their weights
 // that is cut so that all CTAs end together (LINE[c] .. LINE[c + 1] for CTA
 // c), inside a unit's keys where it falls there.
 constexpr int kStage = 64;
 constexpr int kBlock = 128;
-constexpr int kTileRows = 256;
+constexpr int kTile = 128;           // rows of a tile
+constexpr int kTileRows = 2 * kTile;  // rows of a unit
 constexpr int kFewCtasPerSm = 2;
 constexpr int kMaxCtas = 511;
 
@@ -45,11 +47,11 @@ constexpr int kLine = 16;
 constexpr int kJoin = kLine + kMaxCtas + 1;
 constexpr int kJoinInts = 8;
 constexpr int kHdr = kJoin + 3 * kMaxCtas * kJoinInts + 8;
-constexpr int kEnt = 8;
+constexpr int kEnt = 16;
 enum : int {
-  J_ROW = 0,    // packed row of the unit's first row
-  J_ROWS = 1,   // its rows, 0: one CTA has the unit to itself
-  J_HEAD = 2,
+  J_ROW = 0,    // packed row of the unit's first token
+  J_TOKENS = 1,  // its tokens, 0: one CTA has the unit to itself
+  J_HEAD = 2,   // its first head
   J_PART = 3,   // slot of its first part; the others are 2 c, c from ...
   J_CTA = 4,    // ... this CTA on
   J_PARTS = 5   // parts, the first one included
@@ -74,8 +76,13 @@ enum : int {
   E_FULL = 3,     // weight of a unit with two row tiles
   E_LAST = 4,     // weight of a unit of the last tile pair
   E_FIRST = 5,    // the line's place at which those on it start
-  E_LINE = 6      // (64 bits) the line's place at which the stream's units
+  E_LINE = 6,     // (64 bits) the line's place at which the stream's units
                   // would start, had all of them been on it
+  E_TKV = 8,      // tokens of the stream
+  E_TROWS = 9,    // its new tokens
+  E_TQ0 = 10,     // their first packed row
+  E_CHUNK = 11,
+  E_WINDOW = 12
 };
 
 // Weight of a stream's units before its unit n (the last tile pair, which
@@ -121,6 +128,19 @@ inline bool few_mode(const wan_paged_t* c) {
   return static_cast<int64_t>(c->max_new) * (c->heads / c->kv_heads) <=
          kFewRows;
 }
+
+// Query heads of one key head that share a row tile: the most, up to 16, that
+// divide them.  Short streams then fill their tiles and read their keys once
+// for all of them; where the tile does not come out even (5 heads x 25 tokens
+// are 125 rows) long ones would only lose rows.
+inline int tile_pack(const wan_paged_t* c) {
+  const int group = c->heads / c->kv_heads;
+  int p = 1;
+  for (int i = 2; i <= 16; ++i)
+    if (group % i == 0) p = i;
+  return kTile % p != 0 && c->max_new > 1024 ? 1 : p;
+}
+inline int tile_tokens(const wan_paged_t* c) { return kTile / tile_pack(c); }
 
 // Checks of the sizes and of the pointers every call needs.
 int check_cache(const wan_paged_t* c);

@@ -32,7 +32,22 @@ struct PagedArgs {
   int group;           // query heads of one key head
   int page_shift;
   int box_shift;       // rows of one TMA box, min(page_size, 64)
+  int pack, tile_tokens;  // heads and tokens of a row tile
+  uint32_t pack_inv;   // ceil(2^16 / pack)
 };
+
+// TMA: 3-D tiled bulk tensor load into shared memory.
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map,
+                                            uint64_t* bar, int c0, int c1,
+                                            int c2) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::"
+      "complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(
+          smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0),
+      "r"(c1), "r"(c2)
+      : "memory");
+}
 
 // Page of position pos of a stream, as a tensor-map coordinate.
 __device__ __forceinline__ int page_of(const PagedArgs& a, int stream,
@@ -66,13 +81,6 @@ __device__ __forceinline__ const int32_t* find_entry(const int32_t* work,
     first += 31 - __clz(at);
   }
   return list + pg::kEnt * first;
-}
-
-// Keys of a stream that its table can hold.
-__device__ __forceinline__ int keys_of(const PagedArgs& a, int stream) {
-  const int64_t most = static_cast<int64_t>(a.c.max_pages) << a.page_shift;
-  const int kv = max(__ldg(a.c.kv_lens + stream), 0);
-  return kv < most ? kv : static_cast<int>(most);
 }
 
 // Waits until the kernel before this one on the stream has finished (the
@@ -199,7 +207,7 @@ __device__ __forceinline__ List read_list(const PagedArgs& a) {
   List t;
   const int lane = threadIdx.x & 31;
   const int4* e = reinterpret_cast<const int4*>(a.c.work + pg::kHdr) +
-                  2 * min(lane, a.c.n_streams - 1);
+                  pg::kEnt / 4 * min(lane, a.c.n_streams - 1);
   t.e0 = __ldg(e);
   t.e1 = __ldg(e + 1);
   return t;
@@ -228,11 +236,12 @@ __device__ __forceinline__ Segment segment_at(const PagedArgs& a,
   }
   Segment s;
   s.stream = e0.x;
-  const int n = e0.z;
+  // (at least one stage, so that the walk ends whatever the list holds)
+  const int n = max(e0.z, 1);
   const int local = x - e0.y * kvh;
   s.head = local / n;
   const int at = local - s.head * n;
-  s.n = min(n - at, x1 - x);
+  s.n = max(min(n - at, x1 - x), 1);
   s.whole = s.n == n;
   s.stage0 = e0.w + at;
   s.kv = e1.x;
@@ -651,8 +660,11 @@ __global__ void __launch_bounds__(128)
 // per 64-channel half, one lane of the producer warp per box, the block
 // table entry of the next block fetched while this one loads.  One
 // persistent CTA per SM walks its share of the plan's division: rounds of
-// whole units (256 rows of a stream, head), then its part of the line of the
-// last units, so that all CTAs end together whatever the streams' lengths.
+// whole units (two row tiles of a stream and head group), then its part of
+// the line of the last units, so that all CTAs end together whatever the
+// streams' lengths.  The producer warp works the units out ahead and hands
+// them to the others through a ring in shared memory.  Query heads of one key
+// head share a tile (row r: token r / pack, head r % pack).
 // A unit whose rows fit one tile gives both tiles the same Q rows and every
 // other key block: the two softmax chains still hide each other (one chain
 // alone takes about 1 us a block), and the halves are joined at the end.
@@ -678,7 +690,9 @@ enum : int {
   OFINAL = PREADY + QT,    // per tile: a unit's last P V done
   TFREE = OFINAL + QT,     // per tile: O read and Q buffer free (4 warps)
   HALF1 = TFREE + QT,      // tile 1's half of a shared unit is done (4 warps)
-  DRAIN = HALF1 + 1,
+  UFULL = HALF1 + 1,       // unit ring
+  UEMPTY = UFULL + 4,      //   (9 warps have read the unit)
+  DRAIN = UEMPTY + 4,
   NBAR
 };
 
@@ -688,11 +702,14 @@ struct Walk {
   int k, x;
 };
 
+constexpr int kUnits = 4;  // unit ring
+
 struct Unit {
-  int stream, head;
-  int q0;            // packed row of the tile pair's first row
-  int rows;          // its rows, at most 256
-  int a0;            // their first position
+  int stream;        // -1: the CTA's share ends here
+  int head;          // first query head
+  int q0;            // packed row of the first token
+  int tokens;        // at most two tiles of them
+  int a0;            // the first one's position
   int kv, chunk, window;
   int lo, hi;        // keys that any of the rows sees
   int kb0, nblk;     // key blocks of the part (may be none)
@@ -741,7 +758,7 @@ __device__ __forceinline__ bool unit_at(const PagedArgs& a, const Walk& w,
     if (w.x >= x1) return false;
     // the stream whose units hold place x, and the place among them
     e = find_entry(work, active, pg::E_FIRST, 1, w.x);
-    const int tiles = __ldg(e + pg::E_COUNT);
+    const int tiles = max(__ldg(e + pg::E_COUNT), 1);
     const int full = __ldg(e + pg::E_FULL), last = __ldg(e + pg::E_LAST);
     const int64_t y =
         w.x - __ldg(reinterpret_cast<const long long*>(e + pg::E_LINE));
@@ -756,29 +773,31 @@ __device__ __forceinline__ bool unit_at(const PagedArgs& a, const Walk& w,
       weight = full;
     }
     local = head * tiles + tile;
-    t.span = min(weight - off, x1 - w.x);
+    // (at least one place, so that the walk ends whatever the list holds)
+    t.span = max(min(weight - off, x1 - w.x), 1);
     s0 = off;
     s1 = off + t.span;
     if (t.span < weight) t.slot = 2 * blockIdx.x + (w.x == x0 ? 0 : 1);
   }
   t.stream = __ldg(e + pg::E_STREAM);
   const int tiles = __ldg(e + pg::E_COUNT);
-  t.head = local / tiles;
-  const int tx = tiles - 1 - (local - t.head * tiles);
-  const int ql = __ldg(a.c.q_lens + t.stream);
-  t.kv = keys_of(a, t.stream);
-  const int4 cfg = __ldg(reinterpret_cast<const int4*>(a.c.streams) + t.stream);
-  t.chunk = cfg.z;
-  t.window = cfg.w;
-  t.q0 = __ldg(a.c.q_start + t.stream) + tx * pg::kTileRows;
-  t.rows = min(ql - tx * pg::kTileRows, pg::kTileRows);
-  t.a0 = t.kv - ql + tx * pg::kTileRows;
+  const int hgroup = local / tiles;
+  const int tx = tiles - 1 - (local - hgroup * tiles);
+  t.head = hgroup * a.pack;
+  const int pair = 2 * a.tile_tokens;
+  const int ql = __ldg(e + pg::E_TROWS);
+  t.kv = __ldg(e + pg::E_TKV);
+  t.chunk = __ldg(e + pg::E_CHUNK);
+  t.window = __ldg(e + pg::E_WINDOW);
+  t.q0 = __ldg(e + pg::E_TQ0) + tx * pair;
+  t.tokens = min(ql - tx * pair, pair);
+  t.a0 = t.kv - ql + tx * pair;
   t.lo = pg::key_lo(max(t.a0, 0), t.chunk, t.window);
-  t.hi = pg::key_hi(t.a0 + t.rows - 1, t.chunk, t.kv);
+  t.hi = pg::key_hi(t.a0 + t.tokens - 1, t.chunk, t.kv);
   const int b0 = t.lo / BN;
   const int nb = max((t.hi + BN - 1) / BN - b0, 0);
   t.kb0 = b0 + cut(nb, s0, weight);
-  t.nblk = t.rows > 0 ? b0 + cut(nb, s1, weight) - t.kb0 : 0;
+  t.nblk = t.tokens > 0 ? b0 + cut(nb, s1, weight) - t.kb0 : 0;
   return true;
 }
 
@@ -792,6 +811,7 @@ __global__ void __launch_bounds__(wan::kThreads, 1)
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
   __shared__ float2 s_half[BM];  // tile 1's (row max, row sum), shared units
+  __shared__ Unit s_unit[kUnits];
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   if (__ldg(args.c.work + pg::H_MODE) != pg::kModeTile ||
@@ -824,6 +844,10 @@ __global__ void __launch_bounds__(wan::kThreads, 1)
       mbar_init(&bar[TFREE + t], 4);
     }
     mbar_init(&bar[HALF1], 4);
+    for (int i = 0; i < kUnits; ++i) {
+      mbar_init(&bar[UFULL + i], 1);
+      mbar_init(&bar[UEMPTY + i], 9);
+    }
     mbar_init(&bar[DRAIN], 1);
     fence_mbar_init();
   }
@@ -850,11 +874,25 @@ __global__ void __launch_bounds__(wan::kThreads, 1)
       bool ok = true;
       int nq = 0, nq1 = 0;  // units of tile 0, of tile 1
       int nk = 0, nv = 0;   // K and V tiles issued
-      Unit c;
-      for (Walk w = walk_begin(args); ok && unit_at(args, w, c);) {
+      const uint32_t q_bytes = 256u * args.pack * args.tile_tokens;
+      Walk w = walk_begin(args);
+      for (int nu = 0; ok; ++nu) {
+        Unit c;
+        if (!unit_at(args, w, c)) c.stream = -1;
+        const int us = nu % kUnits;
+        if (nu >= kUnits)
+          ok = wait_warp(&bar[UEMPTY + us], (nu / kUnits - 1) & 1, abort_flag,
+                         status);
+        if (!ok) break;
+        if (lane == 0) {
+          s_unit[us] = c;
+          mbar_arrive(&bar[UFULL + us]);
+        }
+        __syncwarp();
+        if (c.stream < 0) break;
         walk_next(args, w, c.span);
         if (c.nblk == 0) continue;
-        const bool two = c.rows > BM;
+        const bool two = c.tokens > args.tile_tokens;
         int64_t pos = static_cast<int64_t>(c.kb0) * BN + row0;
         int page = lane < boxes ? page_of(args, c.stream, pos) : 0;
         if (nq > 0)
@@ -863,12 +901,12 @@ __global__ void __launch_bounds__(wan::kThreads, 1)
           ok = wait_warp(&bar[TFREE + 1], (nq1 - 1) & 1, abort_flag, status);
         if (!ok) break;
         if (leader) {
-          mbar_expect_tx(&bar[QFULL], two ? QT * TILE : TILE);
+          mbar_expect_tx(&bar[QFULL], two ? QT * q_bytes : q_bytes);
           for (int t = 0; t < (two ? QT : 1); ++t) {
-            tma_load_4d(sQ + t * TILE, &tm_q, &bar[QFULL], 0, c.head,
-                        c.q0 + t * BM, 0);
-            tma_load_4d(sQ + t * TILE + HALF, &tm_q, &bar[QFULL], 64, c.head,
-                        c.q0 + t * BM, 0);
+            const int row = c.q0 + t * args.tile_tokens;
+            tma_load_3d(sQ + t * TILE, &tm_q, &bar[QFULL], 0, c.head, row);
+            tma_load_3d(sQ + t * TILE + HALF, &tm_q, &bar[QFULL], 64, c.head,
+                        row);
           }
         }
         ++nq;
@@ -987,11 +1025,17 @@ __global__ void __launch_bounds__(wan::kThreads, 1)
       int g0 = 0;              // ring blocks of earlier units
       int b0 = 0, b1 = 0;      // blocks of each tile in earlier units
       int n0 = 0, n1 = 0;      // units of each tile before this one
-      Unit c;
-      for (Walk w = walk_begin(args); ok && unit_at(args, w, c);) {
-        walk_next(args, w, c.span);
+      for (int nu = 0; ok; ++nu) {
+        const int us = nu % kUnits;
+        ok = wait_warp(&bar[UFULL + us], (nu / kUnits) & 1, abort_flag,
+                       status);
+        if (!ok) break;
+        const Unit c = s_unit[us];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar[UEMPTY + us]);
+        if (c.stream < 0) break;
         if (c.nblk == 0) continue;
-        const bool two = c.rows > BM;
+        const bool two = c.tokens > args.tile_tokens;
         ok = wait_warp(&bar[QFULL], n0 & 1, abort_flag, status);
         if (two) {
           for (int j = 0; j < c.nblk && ok; ++j) {
@@ -1079,30 +1123,39 @@ __global__ void __launch_bounds__(wan::kThreads, 1)
     bool ok = true;
     // phases of this tile's scores, its units and its shared units
     uint32_t sph = 0, uph = 0, hph = 0;
-    for (Walk w = walk_begin(args); ok;) {
-      int nblk, lim_lo = 0, lim_hi = INT32_MAX;
+    // token and head of this thread's row in a tile
+    const int tok_r = static_cast<int>((r * args.pack_inv) >> 16);
+    for (int nu = 0; ok; ++nu) {
+      const int us = nu % kUnits;
+      const Unit& c = s_unit[us];
+      ok = wait_warp(&bar[UFULL + us], (nu / kUnits) & 1, abort_flag, status);
+      if (!ok || c.stream < 0) break;
+      // this warp has read the unit for the last time
+      auto done_with_unit = [&]() {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar[UEMPTY + us]);
+      };
+      int nblk = c.nblk, lim_lo = 0, lim_hi = INT32_MAX;
       int key_step = BN;  // keys from one of this tile's blocks to the next
       {
-        Unit c;
-        if (!unit_at(args, w, c)) break;
-        nblk = c.nblk;
-        int row = t * BM + r;
-        if (c.rows <= BM) {
+        int tok = t * args.tile_tokens + tok_r;
+        int kb0 = c.kb0;
+        if (c.tokens <= args.tile_tokens) {
           if (nblk > 1) {  // shared: every other block, the same rows
-            row = r;
+            tok = tok_r;
             nblk = (nblk + 1 - t) >> 1;
             key_step = 2 * BN;
-            c.kb0 += t;
+            kb0 += t;
           } else if (t > 0) {
-            walk_next(args, w, c.span);
+            done_with_unit();
             continue;
           }
         }
-        // rows behind the tile's last take part unmasked, never written
-        if (row < c.rows) {
-          const int a = c.a0 + row;
-          lim_lo = pg::key_lo(max(a, 0), c.chunk, c.window) - c.kb0 * BN;
-          lim_hi = pg::key_hi(a, c.chunk, c.kv) - c.kb0 * BN;
+        // rows of no token take part unmasked and are never written
+        if (tok_r < args.tile_tokens && tok < c.tokens) {
+          const int a = c.a0 + tok;
+          lim_lo = pg::key_lo(max(a, 0), c.chunk, c.window) - kb0 * BN;
+          lim_hi = pg::key_hi(a, c.chunk, c.kv) - kb0 * BN;
         }
       }
       float m_run = -INFINITY;
@@ -1174,12 +1227,7 @@ __global__ void __launch_bounds__(wan::kThreads, 1)
         uph ^= 1;
         tc_fence_after();
       }
-      // Coordinates again instead of holding them through the key loop.
-      asm volatile("" : "+r"(w.k), "+r"(w.x));
-      Unit ce;
-      unit_at(args, w, ce);
-      walk_next(args, w, ce.span);
-      const bool shared = ce.rows <= BM && ce.nblk > 1;
+      const bool shared = c.tokens <= args.tile_tokens && c.nblk > 1;
       float f0 = 1.f, f1 = 0.f;  // factors of the halves of a shared unit
       if (shared) {
         if (t == 1) {
@@ -1187,6 +1235,7 @@ __global__ void __launch_bounds__(wan::kThreads, 1)
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&bar[HALF1]);
+          done_with_unit();
           continue;  // tile 0's warps read O of both and free both
         }
         ok = wait_warp(&bar[HALF1], hph, abort_flag, status);
@@ -1213,8 +1262,18 @@ __global__ void __launch_bounds__(wan::kThreads, 1)
         }
       };
       const int wrow0 = (warp & 3) * 32;  // this warp's rows of the tile
-      const int live = min(ce.rows - t * BM - wrow0,
-                           args.c.token_cap - ce.q0 - t * BM - wrow0);
+      // rows that are written: packed row of the tile's row, or -1
+      const int tok0 = t * args.tile_tokens;
+      const int most = min(min(c.tokens - tok0, args.tile_tokens),
+                           args.c.token_cap - c.q0 - tok0);
+      const int slot = c.slot, head = c.head, row_q = c.q0 + tok0;
+      done_with_unit();
+      auto row_at = [&](int row) -> int64_t {
+        const int tok = static_cast<int>((row * args.pack_inv) >> 16);
+        if (tok >= most) return -1;
+        return static_cast<int64_t>(row_q + tok) * args.c.heads + head +
+               (row - tok * args.pack);
+      };
       uint8_t* stg = sQ + t * TILE;
       // A row's 16 pieces of 16 bytes go to its place in the Q buffer
       // (swizzled by row, as TMA leaves Q), then half-warps store whole
@@ -1223,73 +1282,71 @@ __global__ void __launch_bounds__(wan::kThreads, 1)
         *reinterpret_cast<uint4*>(stg + (piece >> 3) * HALF + r * 128 +
                                   (((piece & 7) ^ (r & 7)) << 4)) = v;
       };
-      auto flush = [&](uint8_t* dst, int64_t row_bytes) {
+      auto flush = [&](auto address) {
         __syncwarp();
+        const int piece = lane & 15;
 #pragma unroll 4
         for (int i = 0; i < 16; ++i) {
-          const int rr = 2 * i + (lane >> 4), piece = lane & 15;
-          const int row = wrow0 + rr;
+          const int row = wrow0 + 2 * i + (lane >> 4);
           const uint4 v = *reinterpret_cast<const uint4*>(
               stg + (piece >> 3) * HALF + row * 128 +
               (((piece & 7) ^ (row & 7)) << 4));
-          if (rr < live)
-            *reinterpret_cast<uint4*>(dst + rr * row_bytes + piece * 16) = v;
+          const int64_t at = row_at(row);
+          if (at >= 0) address(row, at)[piece] = v;
         }
         __syncwarp();
       };
-      if (ce.slot >= 0) {
+      if (slot >= 0) {
         const int64_t prow =
-            static_cast<int64_t>(ce.slot) * pg::kTileRows + t * BM + wrow0;
-        if (lane < live)
-          args.part_ml[prow + lane] = make_float2(m_run, l_run);
+            static_cast<int64_t>(slot) * pg::kTileRows + t * BM;
+        if (row_at(r) >= 0) args.part_ml[prow + r] = make_float2(m_run, l_run);
         if (nblk > 0) {
 #pragma unroll 1
           for (int hc = 0; hc < 2; ++hc) {
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
+            for (int cc = 0; cc < 2; ++cc) {
               float o[32];
-              load_o(hc * 64 + c * 32, o);
+              load_o(hc * 64 + cc * 32, o);
 #pragma unroll
               for (int e = 0; e < 8; ++e)
-                stage(c * 8 + e,
+                stage(cc * 8 + e,
                       make_uint4(__float_as_uint(o[4 * e]),
                                  __float_as_uint(o[4 * e + 1]),
                                  __float_as_uint(o[4 * e + 2]),
                                  __float_as_uint(o[4 * e + 3])));
             }
-            flush(reinterpret_cast<uint8_t*>(args.part_o + prow * HD +
-                                             hc * 64),
-                  HD * 4);
+            flush([&](int row, int64_t) {
+              return reinterpret_cast<uint4*>(args.part_o + (prow + row) * HD +
+                                              hc * 64);
+            });
           }
         }
-      } else {
-        const int64_t row =
-            (static_cast<int64_t>(ce.q0) + t * BM + wrow0) * args.c.heads +
-            ce.head;
-        uint8_t* dst = reinterpret_cast<uint8_t*>(args.o + row * HD);
-        const int64_t row_bytes = static_cast<int64_t>(args.c.heads) * HD * 2;
-        if (nblk == 0) {
-          // no row sees a key (the Q buffer is not this unit's: no staging)
-          for (int i = lane >> 4; i < live; i += 2)
-            *reinterpret_cast<uint4*>(dst + i * row_bytes + (lane & 15) * 16) =
+      } else if (nblk == 0) {
+        // no row sees a key (the Q buffer is not this unit's: no staging)
+        for (int i = lane >> 4; i < 32; i += 2) {
+          const int64_t at = row_at(wrow0 + i);
+          if (at >= 0)
+            reinterpret_cast<uint4*>(args.o + at * HD)[lane & 15] =
                 make_uint4(0, 0, 0, 0);
-          continue;
         }
+      } else {
         const float inv = l_run > 0.f ? 1.0f / l_run : 0.f;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
+        for (int cc = 0; cc < 4; ++cc) {
           float o[32];
-          load_o(c * 32, o);
+          load_o(cc * 32, o);
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            stage(c * 4 + e,
+            stage(cc * 4 + e,
                   make_uint4(
                       pack_bf16x2(o[8 * e] * inv, o[8 * e + 1] * inv),
                       pack_bf16x2(o[8 * e + 2] * inv, o[8 * e + 3] * inv),
                       pack_bf16x2(o[8 * e + 4] * inv, o[8 * e + 5] * inv),
                       pack_bf16x2(o[8 * e + 6] * inv, o[8 * e + 7] * inv)));
         }
-        flush(dst, row_bytes);
+        flush([&](int, int64_t at) {
+          return reinterpret_cast<uint4*>(args.o + at * HD);
+        });
       }
       if (nblk > 0) {
         // O is read and the staging rows too: the next unit's first P V and
@@ -1329,8 +1386,13 @@ __global__ void __launch_bounds__(128)
     const int i = it % pg::kTileRows;
     const int4 r0 = __ldg(recs + 2 * (it / pg::kTileRows));
     const int4 r1 = __ldg(recs + 2 * (it / pg::kTileRows) + 1);
-    const int row = r0.x + i;
-    if (i >= r0.y || row >= args.c.token_cap) continue;
+    const int r = i & (BM - 1);
+    const int in_tile = static_cast<int>((r * args.pack_inv) >> 16);
+    const int tok = (i / BM) * args.tile_tokens + in_tile;
+    const int row = r0.x + tok;
+    if (in_tile >= args.tile_tokens || tok >= r0.y || row >= args.c.token_cap)
+      continue;
+    const int head = r0.z + r - in_tile * args.pack;
     const int32_t* cut = work + pg::kLine + r1.x - 1;
     JoinAcc<4> acc;
     acc.add_all(
@@ -1341,7 +1403,7 @@ __global__ void __launch_bounds__(128)
         },
         // a CTA between the first and the last may have no share of the line
         [&](int k) { return __ldg(cut + k) < __ldg(cut + k + 1); });
-    acc.write(args.o + (static_cast<int64_t>(row) * args.c.heads + r0.z) * HD,
+    acc.write(args.o + (static_cast<int64_t>(row) * args.c.heads + head) * HD,
               lane);
   }
 }
@@ -1445,7 +1507,8 @@ int launch_tile(const void* k_pages, const void* v_pages,
     if (state[dev] != 1) return WAN_EUNSUPPORTED;
   }
   CUtensorMap mq, mk, mv;
-  int st = make_map_bf16(&mq, a.q, 1, a.c.token_cap, a.c.heads, BM);
+  int st = make_map_rows(&mq, a.q, a.c.token_cap, a.c.heads, a.pack,
+                         a.tile_tokens);
   if (st != WAN_OK) return st;
   const int box = 1 << a.box_shift;
   if ((st = make_map_pages(&mk, k_pages, a.c.n_pages, a.c.kv_heads,
@@ -1498,6 +1561,9 @@ int wan_paged_attn(const wan_paged_t* c, const void* q, const void* k_pages,
   a.group = c->heads / c->kv_heads;
   a.page_shift = paged_log2(c->page_size);
   a.box_shift = paged_log2(c->page_size < 64 ? c->page_size : 64);
+  a.pack = paged::tile_pack(c);
+  a.tile_tokens = paged::tile_tokens(c);
+  a.pack_inv = (65536u + a.pack - 1) / a.pack;
   return paged::few_mode(c)
              ? launch_few(k_pages, v_pages, a, sms, as_stream(s))
              : launch_tile(k_pages, v_pages, a, sms, as_stream(s));

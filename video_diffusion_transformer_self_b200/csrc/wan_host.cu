@@ -98,6 +98,26 @@ int make_map_bf16(CUtensorMap* m, const void* base, int B, int L, int heads,
   return r == CUDA_SUCCESS ? WAN_OK : WAN_EINVAL;
 }
 
+int make_map_rows(CUtensorMap* m, const void* base, int L, int heads,
+                  int box_heads, int box_rows) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return WAN_ECUDA;
+  if (box_heads < 1 || box_rows < 1 || box_heads * box_rows > 256)
+    return WAN_EINVAL;
+  cuuint64_t dims[3] = {128, static_cast<cuuint64_t>(heads),
+                        static_cast<cuuint64_t>(L)};
+  cuuint64_t strides[2] = {256, static_cast<cuuint64_t>(heads) * 256};
+  cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_heads),
+                       static_cast<cuuint32_t>(box_rows)};
+  cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+                  const_cast<void*>(base), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? WAN_OK : WAN_EINVAL;
+}
+
 int make_map_pages(CUtensorMap* m, const void* base, int n_pages,
                    int kv_heads, int page_size, int box_rows) {
   EncodeTiledFn fn = encode_fn();

@@ -32,6 +32,11 @@ int resident_grid(const void* kernel, int threads, int dev);
 int make_map_bf16(CUtensorMap* m, const void* base, int B, int L, int heads,
                   int box_rows);
 
+// The same for B = 1 with a box of box_rows tokens x box_heads heads x 64
+// channels, which lands token by token, head by head.
+int make_map_rows(CUtensorMap* m, const void* base, int L, int heads,
+                  int box_heads, int box_rows);
+
 // Tensor map of a [n_pages, kv_heads, page_size, 128] bf16 page pool with a
 // box of box_rows rows x 64 channels of one head of one page (dims: channel,
 // row, head, page), 128-byte swizzle, zero fill past n_pages.
