@@ -161,6 +161,10 @@ __device__ __forceinline__ int find_stream(const int* incl, int n, int x) {
 // The least weight of a piece that a cut leaves (a piece costs its start, its
 // partial result and the join of it, about six key blocks).
 constexpr int kMinPiece = 64;
+// Where there are more CTAs than units, down to a quarter of it for very few
+// units: 2 units of 80 blocks 36 us with 64, 23 with 16; 12 of 260 51 and 45;
+// 72 of 4 blocks 22 with 64, 33 with 16.
+constexpr int kMinPieceIdle = 16;
 
 // Rounds of whole units beyond which the CTAs' loads count as equal.
 constexpr int kManyRounds = 16;
@@ -189,14 +193,9 @@ __device__ void build_few(const PlanArgs& a, int ql, int kv, int q0, int lo,
   const int idx = static_cast<int>(sc >> 40) - on;
   const int base = static_cast<int>(sc & 0xFFFFFFFFFFull) - n;
   if (on) {
-    int32_t* e = work + kHdr + kEnt * idx;
-    e[E_STREAM] = r;
-    e[E_BASE] = base;
-    e[E_COUNT] = n;
-    e[E_STAGE0] = stage0;
-    e[E_KV] = kv;
-    e[E_ROWS] = ql;
-    e[E_Q0] = q0;
+    int4* e = reinterpret_cast<int4*>(work + kHdr + kEnt * idx);
+    e[0] = make_int4(r, base, n, stage0);
+    e[1] = make_int4(kv, ql, q0, 0);
   }
   if (r == T - 1) {
     const int64_t total = static_cast<int64_t>(base + n) * a.c.kv_heads;
@@ -379,25 +378,19 @@ __device__ void build_tiles(const PlanArgs& a, int ql, int kv, int q0,
   __syncthreads();
   if (on) {
     // thread r has stream r here, the entries' threads their place
-    int32_t* e = work + kHdr + kEnt * place;
-    e[E_TKV] = kv;
-    e[E_TROWS] = ql;
-    e[E_TQ0] = q0;
-    e[E_CHUNK] = chunk;
-    e[E_WINDOW] = window;
+    int4* e = reinterpret_cast<int4*>(work + kHdr + kEnt * place);
+    e[E_TKV / 4] = make_int4(kv, ql, q0, chunk);
+    e[E_WINDOW / 4] = make_int4(window, 0, 0, 0);
     mem.e[place] = q0;
   }
   if (mine) {
-    int32_t* e = work + kHdr + kEnt * r;
-    e[E_STREAM] = src;
-    e[E_BASE] = base;
-    e[E_COUNT] = m_tiles;
-    e[E_FULL] = m_full;
-    e[E_LAST] = m_last;
+    int4* e = reinterpret_cast<int4*>(work + kHdr + kEnt * r);
     const int64_t start = static_cast<int64_t>(line_upto - on_line) -
                           static_cast<int64_t>(skipped);
-    e[E_FIRST] = static_cast<int>(line_upto - on_line);
-    *reinterpret_cast<int64_t*>(e + E_LINE) = start;
+    e[0] = make_int4(src, base, m_tiles, m_full);
+    e[1] = make_int4(m_last, static_cast<int>(line_upto - on_line),
+                     static_cast<int>(start & 0xFFFFFFFFll),
+                     static_cast<int>(start >> 32));
     mem.f[r] = m_ql;
     mem.start[r] = start;
     mem.g[r] = static_cast<int>(line_upto);
@@ -408,19 +401,18 @@ __device__ void build_tiles(const PlanArgs& a, int ql, int kv, int q0,
     const float scale = static_cast<float>(s_line) /
                         static_cast<float>(s_lack ? s_lack : 1);
     int end = static_cast<int>(s_line);
+    const int least =
+        K ? kMinPiece
+          : kMinPieceIdle + (kMinPiece - kMinPieceIdle) * min(2 * U, a.sms) / a.sms;
     if (r < G - 1) {
       end = min(end, static_cast<int>(static_cast<float>(lack_upto) * scale));
       if (end < static_cast<int>(s_line)) {
         // the unit it falls into, and no piece too small to pay for itself
         const int i = find_stream(mem.g, n_act, end);
-        const int64_t y = end - mem.start[i];
-        const int full = mem.c[i], last = mem.d[i];
-        const int64_t period =
-            static_cast<int64_t>(mem.b[i] - 1) * full + last;
-        const int rest = static_cast<int>(y % period);
-        const int len = rest < last ? last : full;
-        const int off = rest < last ? rest : (rest - last) % full;
-        if (off < kMinPiece || len - off < kMinPiece)
+        int tile, len, off;
+        unit_of(end - mem.start[i], mem.b[i], mem.c[i], mem.d[i], &tile, &len,
+                &off);
+        if (off < least || len - off < least)
           end += 2 * off < len ? -off : len - off;
       }
     }

@@ -42,7 +42,8 @@ constexpr int kOneWeight = 6;
 constexpr int kUnitWeight = 48;
 
 // work: a header, LINE[0 .. kMaxCtas], kJoinInts ints per unit of the line
-// (at most three rounds of them), then kEnt ints per active stream.
+// (at most three rounds of them), then kEnt ints per active stream (written
+// and read four at a time, in the order of the E_ fields).
 constexpr int kLine = 16;
 constexpr int kJoin = kLine + kMaxCtas + 1;
 constexpr int kJoinInts = 8;
@@ -122,6 +123,36 @@ __host__ __device__ __forceinline__ int key_hi(int a, int chunk, int kv) {
   if (a < 0) return 0;
   const int64_t e = chunk_end(a, chunk);
   return e < kv ? (e > 0 ? static_cast<int>(e) : 0) : kv;
+}
+
+// Unit of a stream that holds place y of its units' weights: its head group
+// (returned), tile pair (0: the last one), weight and the place in it.  There
+// are at most 1,024 groups, so the fp32 quotient is off by at most 1.
+__device__ __forceinline__ int unit_of(int64_t y, int tiles, int full,
+                                       int last, int* tile, int* weight,
+                                       int* off) {
+  const int64_t period = static_cast<int64_t>(tiles - 1) * full + last;
+  int g = static_cast<int>(static_cast<float>(y) /
+                           static_cast<float>(period));
+  int64_t rest = y - g * period;
+  if (rest < 0) {
+    --g;
+    rest += period;
+  } else if (rest >= period) {
+    ++g;
+    rest -= period;
+  }
+  if (rest < last) {
+    *tile = 0;
+    *weight = last;
+    *off = static_cast<int>(rest);
+  } else {
+    const unsigned r = static_cast<unsigned>(rest) - last;
+    *tile = 1 + static_cast<int>(r / full);
+    *weight = full;
+    *off = static_cast<int>(r % full);
+  }
+  return g;
 }
 
 inline bool few_mode(const wan_paged_t* c) {

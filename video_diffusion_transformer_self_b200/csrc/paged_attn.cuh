@@ -700,6 +700,8 @@ enum : int {
 // then place x of the line.
 struct Walk {
   int k, x;
+  int active, ctas, waves;  // of the work list's header
+  int x0, x1;               // the CTA's part of the line
 };
 
 constexpr int kUnits = 4;  // unit ring
@@ -718,23 +720,31 @@ struct Unit {
 };
 
 __device__ __forceinline__ Walk walk_begin(const PagedArgs& a) {
+  const int32_t* work = a.c.work;
+  // {H_MODE, H_ACTIVE, H_TOTAL, H_CTAS}
+  const int4 hdr = __ldg(reinterpret_cast<const int4*>(work));
   Walk w;
   w.k = 0;
-  w.x = __ldg(a.c.work + pg::kLine + blockIdx.x);
+  w.active = hdr.y;
+  w.ctas = hdr.w;
+  w.waves = __ldg(work + pg::H_WAVES);
+  w.x = w.x0 = __ldg(work + pg::kLine + blockIdx.x);
+  w.x1 = __ldg(work + pg::kLine + blockIdx.x + 1);
   return w;
 }
 
-__device__ __forceinline__ void walk_next(const PagedArgs& a, Walk& w,
-                                          int span) {
-  if (w.k < __ldg(a.c.work + pg::H_WAVES))
+__device__ __forceinline__ void walk_next(Walk& w, int span) {
+  if (w.k < w.waves)
     ++w.k;
   else
     w.x += span;
 }
 
 // Key blocks of a unit's nb before place s of its `weight` places.
+// (fp32: 0 and nb at the ends, and neighbours agree on the cut between them)
 __device__ __forceinline__ int cut(int nb, int s, int weight) {
-  return static_cast<int>(static_cast<int64_t>(nb) * s / weight);
+  return static_cast<int>(static_cast<float>(nb) *
+                          (static_cast<float>(s) / static_cast<float>(weight)));
 }
 
 // The part at w; false at the end of the CTA's share.
@@ -742,42 +752,30 @@ __device__ __forceinline__ bool unit_at(const PagedArgs& a, const Walk& w,
                                         Unit& t) {
   const int32_t* work = a.c.work;
   const int32_t* e;
-  const int active = __ldg(work + pg::H_ACTIVE);
   int local, s0 = 0, s1 = 1, weight = 1;
   t.slot = -1;
   t.span = 0;
-  if (w.k < __ldg(work + pg::H_WAVES)) {
-    const int ctas = __ldg(work + pg::H_CTAS);
+  if (w.k < w.waves) {
     const int c = blockIdx.x;
-    const int u = w.k * ctas + (w.k & 1 ? ctas - 1 - c : c);
-    e = find_entry(work, active, pg::E_BASE, 1, u);
+    const int u = w.k * w.ctas + (w.k & 1 ? w.ctas - 1 - c : c);
+    e = find_entry(work, w.active, pg::E_BASE, 1, u);
     local = u - __ldg(e + pg::E_BASE);
   } else {
-    const int x0 = __ldg(work + pg::kLine + blockIdx.x);
-    const int x1 = __ldg(work + pg::kLine + blockIdx.x + 1);
-    if (w.x >= x1) return false;
+    if (w.x >= w.x1) return false;
     // the stream whose units hold place x, and the place among them
-    e = find_entry(work, active, pg::E_FIRST, 1, w.x);
+    e = find_entry(work, w.active, pg::E_FIRST, 1, w.x);
     const int tiles = max(__ldg(e + pg::E_COUNT), 1);
     const int full = __ldg(e + pg::E_FULL), last = __ldg(e + pg::E_LAST);
     const int64_t y =
         w.x - __ldg(reinterpret_cast<const long long*>(e + pg::E_LINE));
-    const int64_t period = static_cast<int64_t>(tiles - 1) * full + last;
-    const int head = static_cast<int>(y / period);
-    const int rest = static_cast<int>(y - head * period);
-    int tile = 0, off = rest;
-    weight = last;
-    if (rest >= last) {
-      tile = 1 + (rest - last) / full;
-      off = (rest - last) % full;
-      weight = full;
-    }
+    int tile, off;
+    const int head = pg::unit_of(y, tiles, full, last, &tile, &weight, &off);
     local = head * tiles + tile;
     // (at least one place, so that the walk ends whatever the list holds)
-    t.span = max(min(weight - off, x1 - w.x), 1);
+    t.span = max(min(weight - off, w.x1 - w.x), 1);
     s0 = off;
     s1 = off + t.span;
-    if (t.span < weight) t.slot = 2 * blockIdx.x + (w.x == x0 ? 0 : 1);
+    if (t.span < weight) t.slot = 2 * blockIdx.x + (w.x == w.x0 ? 0 : 1);
   }
   t.stream = __ldg(e + pg::E_STREAM);
   const int tiles = __ldg(e + pg::E_COUNT);
@@ -852,6 +850,18 @@ __global__ void __launch_bounds__(wan::kThreads, 1)
     fence_mbar_init();
   }
   if (warp == 9) tmem_alloc(&s_tmem, TMEM_COLS);
+  // the first unit is worked out while tensor memory is allocated
+  Walk w;
+  Unit u0;
+  if (warp == 8) {
+    w = walk_begin(args);
+    if (!unit_at(args, w, u0)) u0.stream = -1;
+    if (lane == 0) {
+      prefetch_tmap(&tm_q);
+      prefetch_tmap(&tm_k);
+      prefetch_tmap(&tm_v);
+    }
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -862,11 +872,6 @@ __global__ void __launch_bounds__(wan::kThreads, 1)
     if (warp == 8) {
       // ---------------------------------------------------- TMA producer --
       const bool leader = elect_one();
-      if (leader) {
-        prefetch_tmap(&tm_q);
-        prefetch_tmap(&tm_k);
-        prefetch_tmap(&tm_v);
-      }
       const int boxes = BN >> args.box_shift;
       const uint32_t box_bytes = 128u << args.box_shift;
       const int in_mask = (1 << args.page_shift) - 1;
@@ -875,10 +880,9 @@ __global__ void __launch_bounds__(wan::kThreads, 1)
       int nq = 0, nq1 = 0;  // units of tile 0, of tile 1
       int nk = 0, nv = 0;   // K and V tiles issued
       const uint32_t q_bytes = 256u * args.pack * args.tile_tokens;
-      Walk w = walk_begin(args);
+      Unit c = u0;
       for (int nu = 0; ok; ++nu) {
-        Unit c;
-        if (!unit_at(args, w, c)) c.stream = -1;
+        if (nu > 0 && !unit_at(args, w, c)) c.stream = -1;
         const int us = nu % kUnits;
         if (nu >= kUnits)
           ok = wait_warp(&bar[UEMPTY + us], (nu / kUnits - 1) & 1, abort_flag,
@@ -890,7 +894,7 @@ __global__ void __launch_bounds__(wan::kThreads, 1)
         }
         __syncwarp();
         if (c.stream < 0) break;
-        walk_next(args, w, c.span);
+        walk_next(w, c.span);
         if (c.nblk == 0) continue;
         const bool two = c.tokens > args.tile_tokens;
         int64_t pos = static_cast<int64_t>(c.kb0) * BN + row0;
@@ -1252,10 +1256,12 @@ __global__ void __launch_bounds__(wan::kThreads, 1)
       // 32 columns of O, the halves joined
       auto load_o = [&](int col, float (&o)[32]) {
         tmem_ld32(o_col + col, o);
-        tmem_ld_wait32(o);
-        if (shared) {
+        if (!shared) {
+          tmem_ld_wait32(o);
+        } else {
           float o1[32];
           tmem_ld32(o_col + 128 + col, o1);
+          tmem_ld_wait32(o);
           tmem_ld_wait32(o1);
 #pragma unroll
           for (int e = 0; e < 32; ++e) o[e] = o[e] * f0 + o1[e] * f1;
