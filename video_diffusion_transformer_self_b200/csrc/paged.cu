@@ -48,9 +48,9 @@ namespace {
 
 // ------------------------------------------------------------- the plan --
 //
-// Bound by a launch and the chain of scans: 76 KB to 2 MB move in 7 to 12 us
-// (1 stream x 4,685 records 7.1 us, 48 streams x 114,041 records 11.8, 777 x
-// 6,348 12.1; 2 us of each is the caller's copy of the state in those runs).
+// Bound by a launch and the chain of scans: 76 KB to 2 MB move in 8 to 14 us
+// (1 stream x 4,685 records 8.0 us, 48 streams x 114,041 records 12.6, 777 x
+// 6,348 13.8; 2 us of each is the caller's copy of the state in those runs).
 // One cluster of CTAs.  Every CTA reads all streams (one thread a stream)
 // and finds the same prefix sums; the moves of pages and the tokens' records
 // are then spread over the threads of all CTAs, each finding its stream by a
@@ -61,10 +61,11 @@ namespace {
 // the pages going out, so no second launch is needed and no CTA waits for
 // another kernel.
 // Threads of a CTA, T below: at least one a stream and one an SM.  Every warp
-// runs the scans, so up to 64 streams take 256 threads (4,685 records of one
-// stream: 7.1 us against 9.8 with 1,024; 32 streams, 23,243 records: 12.1 and
-// 13.4; 100 streams: 16.2 and 16.1; 256: 11.4 and 10.5), more streams or
-// records 1,024.
+// runs the scans, so up to 64 streams take 256 threads, more streams or
+// records 1,024.  Measured against each other when that was chosen: 4,685
+// records of one stream 7.1 us with 256 and 9.8 with 1,024; 32 streams,
+// 23,243 records 12.1 and 13.4; 100 streams 16.2 and 16.1; 256 streams 11.4
+// and 10.5.
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanThreadsFew = 256;
 constexpr int kPlanStreamsFew = 64;
@@ -403,7 +404,8 @@ __device__ void build_tiles(const PlanArgs& a, int ql, int kv, int q0,
     int end = static_cast<int>(s_line);
     const int least =
         K ? kMinPiece
-          : kMinPieceIdle + (kMinPiece - kMinPieceIdle) * min(2 * U, a.sms) / a.sms;
+          : kMinPieceIdle +
+                (kMinPiece - kMinPieceIdle) * min(2 * U, a.sms) / a.sms;
     if (r < G - 1) {
       end = min(end, static_cast<int>(static_cast<float>(lack_upto) * scale));
       if (end < static_cast<int>(s_line)) {
@@ -692,11 +694,12 @@ __global__ void __launch_bounds__(T)
 // is read twice (the second time from L2).  One item a warp and as many CTAs
 // as that takes, two warps each: new CTAs load while others store, where a
 // warp that walked several items alternated between the two.  43,200 rows x
-// 40 heads, 2.65 GB: 398 us, 6.7 TB/s (4-warp CTAs 403, walking 446; 12 warps
-// an SM instead of 16: 499 us).  4,680 rows x 12 heads, 86 MB: 14.4 us out of
-// L2, 20.4 after other traffic (a plain copy of as much: 9.5 and 15.4), bound
+// 40 heads, 2.65 GB: 400 us, 6.6 TB/s (4-warp CTAs 403, walking 446; 12 warps
+// an SM instead of 16: 499 us).  4,680 rows x 12 heads, 86 MB: 13.6 us out of
+// L2, 20.6 after other traffic (a plain copy of as much: 9.5 and 15.4), bound
 // by the latency of a warp's chain (record, row, weights) over 3.3 rounds of
-// CTAs.
+// CTAs; two or three rows a warp took 15 to 23 us there, the weights fetched
+// ahead of the row 18.9.
 constexpr int kWrThreads = 64;
 constexpr int kWrWarps = kWrThreads / 32;
 constexpr int kWrMaxRows = 20;

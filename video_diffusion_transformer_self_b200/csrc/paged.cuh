@@ -21,10 +21,10 @@ constexpr int kModeNone = 0, kModeFew = 1, kModeTile = 2;
 // kTile: a row tile holds tile_tokens() tokens x tile_pack() query heads of
 // one key head.  Units are (tile pair, tile_pack() heads), numbered streams by
 // falling length, then heads, then tile pair (the stream's last one first: it
-// sees the most keys).  H_WAVES rounds of one whole unit per CTA come first, in turn
-// up and down the CTAs; the units behind them form a line of their weights
-// that is cut so that all CTAs end together (LINE[c] .. LINE[c + 1] for CTA
-// c), inside a unit's keys where it falls there.
+// sees the most keys).  H_WAVES rounds of one whole unit per CTA come first,
+// in turn up and down the CTAs; the units behind them form a line of their
+// weights that is cut so that all CTAs end together (LINE[c] .. LINE[c + 1]
+// for CTA c), inside a unit's keys where it falls there.
 constexpr int kStage = 64;
 constexpr int kBlock = 128;
 constexpr int kTile = 128;           // rows of a tile

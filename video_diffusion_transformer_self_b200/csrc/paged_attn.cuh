@@ -174,8 +174,8 @@ struct JoinAcc {
 // items.  Two CTAs per SM keep up to 192 KB in flight.  An item that several
 // CTAs share is written as partial results (at most two per CTA) and joined
 // by paged_few_join.  Measured, join included: 24 streams x 8 key heads x
-// 32,760 keys (3.2 GB) 488 us, 6.6 TB/s; 24 ragged streams (689 MB) 120 us,
-// 5.8 TB/s; 1 token x 12 heads x 7,800 keys (48 MB) 13.6 us, 5.3 of them two
+// 32,760 keys (3.2 GB) 488 us, 6.6 TB/s; 24 ragged streams (689 MB) 122 us,
+// 5.6 TB/s; 1 token x 12 heads x 7,800 keys (48 MB) 13.8 us, 5.3 of them two
 // launches and the chain work list -> block table -> keys.
 namespace few {
 constexpr int kWarps = 4;
@@ -664,7 +664,8 @@ __global__ void __launch_bounds__(128)
 // the line of the last units, so that all CTAs end together whatever the
 // streams' lengths.  The producer warp works the units out ahead and hands
 // them to the others through a ring in shared memory.  Query heads of one key
-// head share a tile (row r: token r / pack, head r % pack).
+// head share a tile (row r: token r / pack, head r % pack), so their keys
+// are read once: 6 streams x 40 heads over 8 x 43 to 86 rows 47 -> 22.4 us.
 // A unit whose rows fit one tile gives both tiles the same Q rows and every
 // other key block: the two softmax chains still hide each other (one chain
 // alone takes about 1 us a block), and the halves are joined at the end.
@@ -675,9 +676,12 @@ __global__ void __launch_bounds__(128)
 // fp32 partial results instead, joined by paged_tile_join.
 // Bound, like attn_fwd_kernel, by each tile's chain of softmax and matrix
 // products (tensor pipe 61 % active), and by the power cap in long calls.
-// Measured: 4,680 rows x 12 heads over 32,760 keys 735 to 870 us by clock
-// (1,080 to 1,280 TFLOP/s), x 40 heads over 65,520 keys 5.05 to 5.8 ms (1,076
-// to 1,243); with units of 256 rows a CTA in turn they took 965 us and 6.0 ms.
+// Measured: 4,680 rows x 12 heads over 32,760 keys 740 to 860 us by clock
+// (1,095 to 1,270 TFLOP/s), x 40 heads over 65,520 keys 5.0 to 5.6 ms (1,120
+// to 1,250); with units of 256 rows a CTA in turn they took 965 us and 6.0 ms.
+// Rows stored from registers instead of through the Q buffer, the next unit's
+// scores started meanwhile: small calls 4 % shorter to 6 % longer, long ones
+// unchanged, two to three registers spilled.
 namespace tile {
 enum : int {
   QFULL = 0,
