@@ -233,6 +233,48 @@ def test_same_result_every_time_and_in_a_graph(max_new, new):
         assert_attn(f64(got)[rows], ref, mag, "replay", 30.0)
 
 
+def test_a_graph_keeps_its_workspace_when_max_new_grows():
+    """A captured single-token step goes on using the scratch it was captured
+    with after steps that need more: what is allocated later stays whole."""
+    streams = [(8, 8, 64, 0)] * 2
+    cap = 32
+    c, oc = make(streams, (60, 8, 8), 100, 32, 60, 2, 2, cap, 16)
+    for _ in range(12):                    # three key stages a stream
+        step(c, oc, [16, 15])
+    kp, vp = c.new_pools()
+    kp.normal_()
+    vp.normal_()
+    q = rows_bf16(cap, 2, 11).cuda()
+    o = torch.zeros_like(q)
+    small = c.workspace()
+    size = small.numel()
+    lens = torch.ones(2, dtype=torch.int32, device="cuda")
+    saved = c.state.clone()
+    c.plan(lens)
+    c.attn(q, kp, vp, o)
+    first = o.clone()
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        c.plan(lens)
+        c.attn(q, kp, vp, o)
+    at = small.data_ptr()
+    del small
+    c.max_new = 700
+    assert c.workspace().numel() > size
+    later = [torch.full((size,), 77, dtype=torch.uint8, device="cuda")
+             for _ in range(4)]
+    c.state.copy_(saved)
+    o.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(o, first)
+    for t in later:
+        assert bool((t == 77).all())
+    c.max_new = 16
+    assert c.workspace().data_ptr() == at
+
+
 def test_write_and_attention_over_layers_match_the_whole_video():
     """Three chunks of a video through plan, write and attention of two
     layers give what the contiguous calls give on the whole video."""

@@ -110,7 +110,8 @@ class PagedCache:
         if self._table_bytes == 0:
             raise ValueError("grid %r has no RoPE table" % (grid,))
         self._desc = None
-        self._workspace = self._need_for = self._planned = None
+        self._workspaces = {}
+        self._need_for = self._planned = None
         self._q_shape = torch.Size((self.token_cap, self.heads, 128))
         self._kv_shape = torch.Size((self.token_cap, self.kv_heads, 128))
         self._pool_shape = torch.Size((self.n_pages, self.kv_heads,
@@ -218,14 +219,16 @@ class PagedCache:
         return self._need
 
     def workspace(self):
-        """The cache's own scratch (allocated anew if another max_new needs
-        more).  Calls that overlap on the device need one each (``attn``'s
-        workspace argument)."""
+        """The cache's own scratch: one for each of the two sizes that a
+        max_new can need, kept for the cache's life, since captured graphs
+        go on using the one they were captured with.  Calls that overlap on
+        the device need one each (``attn``'s workspace argument)."""
         need = self.workspace_bytes()
-        if self._workspace is None or self._workspace.numel() < need:
-            self._workspace = torch.empty(need, dtype=torch.uint8,
-                                          device=self.device)
-        return self._workspace
+        buf = self._workspaces.get(need)
+        if buf is None:
+            buf = self._workspaces[need] = torch.empty(
+                need, dtype=torch.uint8, device=self.device)
+        return buf
 
     def attn(self, q, k_pages, v_pages, o, softmax_scale=None, stream=None,
              workspace=None):
