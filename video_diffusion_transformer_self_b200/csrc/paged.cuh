@@ -127,10 +127,12 @@ __host__ __device__ __forceinline__ int key_hi(int a, int chunk, int kv) {
 
 // Unit of a stream that holds place y of its units' weights: its head group
 // (returned), tile pair (0: the last one), weight and the place in it.  There
-// are at most 1,024 groups, so the fp32 quotient is off by at most 1.
-__device__ __forceinline__ int unit_of(int64_t y, int tiles, int full,
-                                       int last, int* tile, int* weight,
-                                       int* off) {
+// are at most 1,024 groups, so the fp32 quotient is off by at most 1.  A
+// group's weights pass 32 bits (16 heads of one key head, 2^20 tokens over as
+// many keys: 2^32), so the place in it is divided in 64.
+__host__ __device__ __forceinline__ int unit_of(int64_t y, int tiles, int full,
+                                                int last, int* tile,
+                                                int* weight, int* off) {
   const int64_t period = static_cast<int64_t>(tiles - 1) * full + last;
   int g = static_cast<int>(static_cast<float>(y) /
                            static_cast<float>(period));
@@ -147,10 +149,12 @@ __device__ __forceinline__ int unit_of(int64_t y, int tiles, int full,
     *weight = last;
     *off = static_cast<int>(rest);
   } else {
-    const unsigned r = static_cast<unsigned>(rest) - last;
-    *tile = 1 + static_cast<int>(r / full);
+    const uint64_t r = static_cast<uint64_t>(rest - last);
+    const uint64_t d = static_cast<uint64_t>(full);
+    const uint64_t n = r / d;
+    *tile = 1 + static_cast<int>(n);
     *weight = full;
-    *off = static_cast<int>(r % full);
+    *off = static_cast<int>(r - n * d);
   }
   return g;
 }
