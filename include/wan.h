@@ -29,7 +29,8 @@
  *   WAN_ECUDA.  Device-side faults surface at the caller's next synchronise.
  * - Every wait inside a kernel is bounded (about two seconds); a wait that
  *   runs out records WAN_ETIMEOUT in a device status word, read and cleared
- *   by wan_device_status().
+ *   by wan_device_status().  wan_paged_attn records WAN_EINVAL there when it
+ *   meets a plan that was made with another descriptor.
  */
 #ifndef WAN_H_
 #define WAN_H_
@@ -397,6 +398,10 @@ int wan_paged_write(const wan_paged_t* c, const void* q, void* q_out,
  * the stream's end, or before its window) may hold anything, NaN included.
  * fp32 softmax and accumulation; the weights are rounded to bf16 for the
  * tensor cores.  o must not alias q or the pools.
+ * The plan in c->work must have been made with the same max_new and heads
+ * (or none at all: nothing is written).  Where it was not, as after replaying
+ * a graph that captured a plan with another max_new, o is left as it was and
+ * the device status word (wan_device_status) becomes WAN_EINVAL.
  * workspace: wan_paged_workspace_bytes(c) bytes of device memory (of the
  * current device; WAN_ENOSPACE if there are fewer), 16-byte aligned,
  * contents free on entry and unspecified on return; calls that share one
@@ -524,7 +529,9 @@ int wan_wait_selftest(int arrive, void* s);
 
 /* ------------------------------------------------------------- status ---
  * Reads (and, if clear != 0, resets) the device status word of the current
- * device: 0 or WAN_ETIMEOUT.  Synchronous (waits for the device).          */
+ * device: 0, WAN_ETIMEOUT (a bounded wait ran out) or WAN_EINVAL (a
+ * wan_paged_attn whose plan was made with another descriptor wrote nothing).
+ * Synchronous (waits for the device).                                      */
 int wan_device_status(int clear);
 
 #ifdef __cplusplus

@@ -1,0 +1,75 @@
+"""What the paged cache does around a step: plans that do not belong to the
+attention call, scratch on other streams, values that are not finite."""
+
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from gpu_common import f64
+from paged_common import (assert_attn, expect_attn, make, rows_bf16, step)
+from video_diffusion_transformer_self_b200 import build, wan
+
+pytestmark = pytest.mark.gpu
+SCALE = 1.0 / math.sqrt(128)
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    build.build()
+    wan.lib()
+
+
+# the kernel, the rows of a key head, the heads of a row tile (5 heads share a
+# tile up to max_new 1,024), each way round
+@pytest.mark.parametrize("heads,kv_heads,graph_max,call_max", [
+    (2, 2, 700, 16), (2, 2, 16, 700), (2, 2, 16, 2), (2, 2, 2, 16),
+    (5, 1, 1100, 300), (5, 1, 300, 1100), (8, 1, 1100, 300)])
+def test_attention_refuses_a_plan_replayed_with_another_max_new(
+        heads, kv_heads, graph_max, call_max):
+    c, oc = make([(8, 8, 64, 0)] * 2, (60, 8, 8), 60, 32, 40, heads, kv_heads,
+                 64, graph_max)
+    lens = torch.tensor([2, 1], dtype=torch.int32, device="cuda")
+    kp, vp = c.new_pools()
+    kp.normal_()
+    vp.normal_()
+    q = rows_bf16(64, heads, 5).cuda()
+    o = rows_bf16(64, heads, 6).cuda()
+    rest = o.clone()
+    saved = c.state.clone()
+    c.plan(lens)                     # first launches outside the capture
+    c.state.copy_(saved)
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        c.plan(lens)
+    c.max_new = call_max
+    c.plan(lens)                     # what the class remembers
+    oc.plan([2, 1])
+    c.attn(q, kp, vp, torch.zeros_like(o))
+    torch.cuda.synchronize()
+    assert wan.device_status() == 0
+    graph.replay()
+    want = oc.plan([2, 1])
+    c.attn(q, kp, vp, o)
+    torch.cuda.synchronize()
+    same = (heads, kv_heads) == (8, 1)   # 8 heads share a tile either way
+    assert wan.device_status() == (0 if same else wan.WAN_EINVAL)
+    assert wan.device_status() == 0      # read and cleared
+    if same:
+        for _, rows, ref, mag in expect_attn(c, oc, q, kp, vp, want, SCALE):
+            assert_attn(f64(o)[rows], ref, mag, "same layout", 30.0)
+        return
+    assert torch.equal(o, rest)
+    # a plan of the call's own kind serves it again
+    c.plan(lens)
+    want = oc.plan([2, 1])
+    c.attn(q, kp, vp, o)
+    torch.cuda.synchronize()
+    assert wan.device_status() == 0
+    for _, rows, ref, mag in expect_attn(c, oc, q, kp, vp, want, SCALE):
+        assert_attn(f64(o)[rows], ref, mag, "planned again", 30.0)
+    taken = np.zeros(64, bool)
+    taken[:3] = True
+    assert np.array_equal(f64(o)[~taken], f64(rest)[~taken])

@@ -9,7 +9,7 @@ import subprocess
 
 import pytest
 
-from video_diffusion_transformer_self_b200 import build
+from video_diffusion_transformer_self_b200 import build, wan
 
 CSRC = os.path.join(build.PKG, "csrc")
 SOURCE = r"""
@@ -20,6 +20,9 @@ extern "C" int unit_of(int64_t y, int tiles, int full, int last, int* tile,
 }
 extern "C" int64_t weight_before(int n, int tiles, int full, int last) {
   return wan::paged::weight_before(n, tiles, full, last);
+}
+extern "C" int work_kind(const wan_paged_t* c) {
+  return wan::paged::work_kind(c);
 }
 extern "C" int pair_weight(int nb) {
   return wan::paged::kPairWeight * nb + wan::paged::kUnitWeight;
@@ -82,3 +85,30 @@ def test_every_place_maps_to_its_unit(units, groups, ql, pair, keys):
                 got = units.unit_of(start + off, tiles, full, last, t, w, o)
                 assert (got, t.value, w.value, o.value) == \
                     (g, tile, size, off), (n, off)
+
+
+def test_work_lists_of_other_layouts_have_other_kinds(units):
+    def kind(heads, kv_heads, max_new):
+        d = wan.PagedDesc()
+        d.heads, d.kv_heads, d.max_new = heads, kv_heads, max_new
+        return units.work_kind(ctypes.byref(d))
+
+    # few rows: their number; tiles: the heads of a tile, which long steps of
+    # groups like 5 and 7 do not share
+    assert kind(8, 8, 16) != kind(8, 8, 17)
+    assert kind(8, 8, 16) != kind(8, 8, 2)
+    assert kind(5, 1, 1024) != kind(5, 1, 1025)
+    assert kind(8, 8, 700) == kind(8, 8, 1 << 27)
+    assert kind(8, 2, 1024) == kind(8, 2, 1025)
+    seen = {}
+    for heads in (1, 2, 7, 8, 40, 512, 1024):
+        for kv_heads in range(1, heads + 1):
+            if heads % kv_heads == 0:
+                group = heads // kv_heads
+                for rows in range(group, 17, group):
+                    k = kind(heads, kv_heads, rows // group)
+                    assert k > 0 and k not in seen
+                    seen[k] = (heads, kv_heads, rows)
+                k = kind(heads, kv_heads, 1 << 20)
+                assert k > 0 and k not in seen
+                seen[k] = (heads, kv_heads, 0)

@@ -75,7 +75,7 @@ struct PlanArgs {
   const int32_t* new_lens;
   int page_shift;
   int sms;
-  int few;
+  int few, kind;
   int pack, tile_tokens;  // of the tile kernel
 };
 
@@ -204,7 +204,7 @@ __device__ void build_few(const PlanArgs& a, int ql, int kv, int q0, int lo,
     // 384 stages: 8.3 us on 192 CTAs, 9.0 on 296)
     const int64_t most = min(max(total / 2, static_cast<int64_t>(a.sms)),
                              static_cast<int64_t>(a.sms) * kFewCtasPerSm);
-    work[H_MODE] = kModeFew;
+    work[H_KIND] = a.kind;
     work[H_ACTIVE] = idx + on;
     work[H_TOTAL] = static_cast<int>(total);
     work[H_CTAS] =
@@ -449,7 +449,7 @@ __device__ void build_tiles(const PlanArgs& a, int ql, int kv, int q0,
     dst[1] = make_int4(rec[4], rec[5], rec[6], rec[7]);
   }
   if (r == 0) {
-    work[H_MODE] = kModeTile;
+    work[H_KIND] = a.kind;
     work[H_ACTIVE] = s_act;
     work[H_TOTAL] = U;
     work[H_CTAS] = G;
@@ -899,6 +899,7 @@ int wan_paged_plan(const wan_paged_t* c, const int32_t* new_lens, void* s) {
   a.sms = device_sms(dev);
   if (a.sms < 1 || a.sms * kFewCtasPerSm > kMaxCtas) return WAN_ECUDA;
   a.few = few_mode(c) ? 1 : 0;
+  a.kind = work_kind(c);
   a.pack = tile_pack(c);
   a.tile_tokens = tile_tokens(c);
   cudaLaunchConfig_t cfg = {};

@@ -14,6 +14,7 @@ constexpr int kMaxStreams = 1024;
 // 16-row tile run on the kernel that streams the cache through mma.sync
 // (kFew); longer ones on the 256-row tcgen05 kernel (kTile).
 constexpr int kFewRows = 16;
+// kModeNone: no plan has been made.
 constexpr int kModeNone = 0, kModeFew = 1, kModeTile = 2;
 
 // kFew: the (stream, key head, 64-key stage) items form one line that is cut
@@ -58,7 +59,7 @@ enum : int {
   J_PARTS = 5   // parts, the first one included
 };
 enum : int {
-  H_MODE = 0,     // kMode*
+  H_KIND = 0,     // work_kind() of the plan's descriptor
   H_ACTIVE = 1,   // entries
   H_TOTAL = 2,    // kFew: stages x key heads; kTile: units
   H_CTAS = 3,     // CTAs that take part
@@ -176,6 +177,17 @@ inline int tile_pack(const wan_paged_t* c) {
   return kTile % p != 0 && c->max_new > 1024 ? 1 : p;
 }
 inline int tile_tokens(const wan_paged_t* c) { return kTile / tile_pack(c); }
+
+// What the work list's layout depends on, in one number that is never
+// kModeNone: the kernel, the heads and, of max_new, the rows of a key head
+// (kFew) or the heads of a row tile (kTile).  The attention reads a list only
+// if its own descriptor gives the number that the plan wrote.
+inline int work_kind(const wan_paged_t* c) {
+  const int mode = few_mode(c) ? kModeFew : kModeTile;
+  const int rows = few_mode(c) ? c->max_new * (c->heads / c->kv_heads)
+                               : tile_pack(c);
+  return mode | rows << 2 | c->heads << 7 | c->kv_heads << 18;
+}
 
 // Checks of the sizes and of the pointers every call needs.
 int check_cache(const wan_paged_t* c);

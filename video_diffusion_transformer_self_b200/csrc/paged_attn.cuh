@@ -34,7 +34,17 @@ struct PagedArgs {
   int box_shift;       // rows of one TMA box, min(page_size, 64)
   int pack, tile_tokens;  // heads and tokens of a row tile
   uint32_t pack_inv;   // ceil(2^16 / pack)
+  int kind;            // the work list's H_KIND
 };
+
+// A work list that was made for another descriptor (another max_new, say, by
+// a graph replayed since) would be read as other heads and tokens, past o
+// even: nothing is written then, and the device status word says so.  Once a
+// call, by the main kernel; a list never planned (zeros) is an empty step.
+__device__ __forceinline__ void report_kind(int kind) {
+  if (blockIdx.x == 0 && threadIdx.x == 0 && kind != pg::kModeNone)
+    atomicCAS(&g_wan_status, 0, WAN_EINVAL);
+}
 
 // TMA: 3-D tiled bulk tensor load into shared memory.
 __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map,
@@ -304,10 +314,14 @@ __global__ void __launch_bounds__(kThreads, pg::kFewCtasPerSm)
   extern __shared__ __align__(128) uint8_t smem_raw[];
   const int32_t* work = args.c.work;
   List list = read_list(args);
-  // {H_MODE, H_ACTIVE, H_TOTAL, H_CTAS}
+  // {H_KIND, H_ACTIVE, H_TOTAL, H_CTAS}
   const int4 hdr = __ldg(reinterpret_cast<const int4*>(work));
   const int cta = blockIdx.x;
-  if (hdr.x != pg::kModeFew || hdr.y < 1 || cta >= hdr.w) return;
+  if (hdr.x != args.kind) {
+    report_kind(hdr.x);
+    return;
+  }
+  if (hdr.y < 1 || cta >= hdr.w) return;
   list.active = hdr.y;
   const pg::Line line(hdr.z, hdr.w);
   const int x0 = line.first(cta), x1 = line.first(cta + 1);
@@ -616,7 +630,7 @@ __global__ void __launch_bounds__(kThreads, pg::kFewCtasPerSm)
 __global__ void __launch_bounds__(128)
     paged_few_join(const __grid_constant__ PagedArgs args) {
   const int32_t* work = args.c.work;
-  if (__ldg(work + pg::H_MODE) != pg::kModeFew) return;
+  if (__ldg(work + pg::H_KIND) != args.kind) return;
   const int kvh = args.c.kv_heads;
   const int rows = min(args.c.max_new * args.group, kRows);
   const int64_t items =
@@ -725,7 +739,7 @@ struct Unit {
 
 __device__ __forceinline__ Walk walk_begin(const PagedArgs& a) {
   const int32_t* work = a.c.work;
-  // {H_MODE, H_ACTIVE, H_TOTAL, H_CTAS}
+  // {H_KIND, H_ACTIVE, H_TOTAL, H_CTAS}
   const int4 hdr = __ldg(reinterpret_cast<const int4*>(work));
   Walk w;
   w.k = 0;
@@ -816,8 +830,12 @@ __global__ void __launch_bounds__(wan::kThreads, 1)
   __shared__ Unit s_unit[kUnits];
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  if (__ldg(args.c.work + pg::H_MODE) != pg::kModeTile ||
-      static_cast<int>(blockIdx.x) >= __ldg(args.c.work + pg::H_CTAS) ||
+  const int kind = __ldg(args.c.work + pg::H_KIND);
+  if (kind != args.kind) {
+    report_kind(kind);
+    return;
+  }
+  if (static_cast<int>(blockIdx.x) >= __ldg(args.c.work + pg::H_CTAS) ||
       __ldg(args.c.work + pg::H_TOTAL) < 1)
     return;
   launch_dependents();
@@ -1384,7 +1402,7 @@ __global__ void __launch_bounds__(wan::kThreads, 1)
 __global__ void __launch_bounds__(128)
     paged_tile_join(const __grid_constant__ PagedArgs args) {
   const int32_t* work = args.c.work;
-  if (__ldg(work + pg::H_MODE) != pg::kModeTile) return;
+  if (__ldg(work + pg::H_KIND) != args.kind) return;
   const int n = __ldg(work + pg::H_TOTAL) -
                 __ldg(work + pg::H_WAVES) * __ldg(work + pg::H_CTAS);
   const int4* recs = reinterpret_cast<const int4*>(work + pg::kJoin);
@@ -1574,6 +1592,7 @@ int wan_paged_attn(const wan_paged_t* c, const void* q, const void* k_pages,
   a.pack = paged::tile_pack(c);
   a.tile_tokens = paged::tile_tokens(c);
   a.pack_inv = (65536u + a.pack - 1) / a.pack;
+  a.kind = paged::work_kind(c);
   return paged::few_mode(c)
              ? launch_few(k_pages, v_pages, a, sms, as_stream(s))
              : launch_tile(k_pages, v_pages, a, sms, as_stream(s));

@@ -233,7 +233,10 @@ class PagedCache:
     def attn(self, q, k_pages, v_pages, o, softmax_scale=None, stream=None,
              workspace=None):
         """o = softmax(q K^T scale) V over the pages for the planned rows
-        (wan_paged_attn)."""
+        (wan_paged_attn).  The last plan on the device must have been made
+        with this max_new: a plan() call with another one is refused here, a
+        graph replayed since leaves o as it was and shows in
+        wan.device_status()."""
         self._check(self._q_shape, "q", q)
         self._check(self._q_shape, "o", o)
         self._check(self._pool_shape, "k_pages", k_pages)

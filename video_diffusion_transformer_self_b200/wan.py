@@ -668,8 +668,9 @@ def wait_selftest(arrive, stream=None):
 
 
 def device_status(clear=True):
-    """0, or WAN_ETIMEOUT if a bounded in-kernel wait ran out."""
+    """0, WAN_ETIMEOUT if a bounded in-kernel wait ran out, or WAN_EINVAL if
+    a paged attention call met a plan made with another descriptor."""
     st = lib().wan_device_status(1 if clear else 0)
-    if st not in (0, WAN_ETIMEOUT):
+    if st not in (0, WAN_ETIMEOUT, WAN_EINVAL):
         _check(st, "wan_device_status")
     return st
