@@ -73,3 +73,26 @@ def test_attention_refuses_a_plan_replayed_with_another_max_new(
     taken = np.zeros(64, bool)
     taken[:3] = True
     assert np.array_equal(f64(o)[~taken], f64(rest)[~taken])
+
+
+def test_no_call_allocates_whatever_max_new_becomes():
+    """Scratch of both kernels exists before the first call: none is taken
+    from the current stream's memory for a call on another stream."""
+    for first, heads, kv_heads in ((16, 2, 2), (700, 2, 2), (1, 40, 2)):
+        c, oc = make([(8, 8, 64, 0)] * 2, (60, 8, 8), 60, 32, 40, heads,
+                     kv_heads, 64, first)
+        kp, vp = c.new_pools()
+        q = rows_bf16(64, heads, 5).cuda()
+        o = torch.zeros_like(q)
+        lens = torch.ones(2, dtype=torch.int32, device="cuda")
+        torch.cuda.synchronize()
+        side = torch.cuda.Stream()
+        before = torch.cuda.memory_stats()["allocation.all.allocated"]
+        for max_new in (first, 700, 16, 1, 3000, 64, 10 ** 9):
+            c.max_new = max_new
+            c.plan(lens, stream=side)
+            c.attn(q, kp, vp, o, stream=side)
+            assert c.workspace().numel() == c.workspace_bytes() > 0
+        assert torch.cuda.memory_stats()["allocation.all.allocated"] == before
+        torch.cuda.synchronize()
+        assert wan.device_status() == 0

@@ -45,6 +45,10 @@ class PagedCache:
     one stream in a step (default token_cap); together with heads / kv_heads
     it picks the attention kernel (max_new may be set anew before a plan).
 
+    The cache's tensors are allocated and filled on the stream that is
+    current here; calls on another one are ordered behind it by the caller,
+    as for any tensor.
+
     state holds everything that a plan carries from step to step in one
     int32 tensor, with the views kv_lens, first_pages, block_table, free_ring
     and ring_state: saving and restoring it takes a step back (pages must
@@ -110,14 +114,22 @@ class PagedCache:
         if self._table_bytes == 0:
             raise ValueError("grid %r has no RoPE table" % (grid,))
         self._desc = None
-        self._workspaces = {}
         self._need_for = self._planned = None
         self._q_shape = torch.Size((self.token_cap, self.heads, 128))
         self._kv_shape = torch.Size((self.token_cap, self.kv_heads, 128))
         self._pool_shape = torch.Size((self.n_pages, self.kv_heads,
                                        self.page_size, 128))
         self.reset()
-        self.workspace()  # not inside a first call that is being captured
+        # Scratch of both sizes that a max_new can need, now: allocated inside
+        # a call it would belong to the current stream while the call may run
+        # on another, or to the graph that is being captured.
+        self._workspaces = {}
+        d = self.descriptor()
+        for d.max_new in (1, 2 ** 31 - 1):
+            need = wan.paged_workspace_bytes(d, dev)
+            if need not in self._workspaces:
+                self._workspaces[need] = torch.empty(need, dtype=torch.uint8,
+                                                     device=dev)
 
     def reset(self):
         """All streams empty, all pages free."""
@@ -220,15 +232,11 @@ class PagedCache:
 
     def workspace(self):
         """The cache's own scratch: one for each of the two sizes that a
-        max_new can need, kept for the cache's life, since captured graphs
-        go on using the one they were captured with.  Calls that overlap on
-        the device need one each (``attn``'s workspace argument)."""
-        need = self.workspace_bytes()
-        buf = self._workspaces.get(need)
-        if buf is None:
-            buf = self._workspaces[need] = torch.empty(
-                need, dtype=torch.uint8, device=self.device)
-        return buf
+        max_new can need, allocated with the cache and kept for its life,
+        since captured graphs go on using the one they were captured with.
+        Calls that overlap on the device need one each (``attn``'s workspace
+        argument)."""
+        return self._workspaces[self.workspace_bytes()]
 
     def attn(self, q, k_pages, v_pages, o, softmax_scale=None, stream=None,
              workspace=None):
