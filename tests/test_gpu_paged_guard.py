@@ -96,3 +96,52 @@ def test_no_call_allocates_whatever_max_new_becomes():
         assert torch.cuda.memory_stats()["allocation.all.allocated"] == before
         torch.cuda.synchronize()
         assert wan.device_status() == 0
+
+
+# one part a row and many (few keys, many keys), both kernels
+@pytest.mark.parametrize("max_new", [4, 300])
+@pytest.mark.parametrize("kv", [30, 5000])
+def test_rows_that_are_not_finite_stay_so_however_they_are_cut(max_new, kv):
+    """A NaN or infinity in a query gives NaN in its row and in no other,
+    whether one CTA has the row's keys or the partial results of many are
+    joined; a NaN key gives NaN in the rows of the few-row kernel that see
+    it."""
+    n = 4
+    c, oc = make([(10, 10, 1, 0)], (60, 10, 10), 330, 16, 330, 2, 2, n,
+                 max_new)
+    c.max_new = max_new
+    c.kv_lens[0] = oc.kv[0] = kv
+    held = -(-kv // 16)
+    pages = list(range(held))
+    c.block_table[0, :held] = torch.arange(held, dtype=torch.int32)
+    oc.table[0][:held] = pages
+    c.ring_state.copy_(torch.tensor([held, 330 - held], dtype=torch.int32))
+    oc.head, oc.count = held, 330 - held
+    want = step(c, oc, [n])
+    kp, vp = c.new_pools()
+    kp.normal_()
+    vp.normal_()
+    q = rows_bf16(n, 2, 5).cuda()
+    o = torch.zeros_like(q)
+    for bad in (float("nan"), float("inf"), -float("inf")):
+        qb = q.clone()
+        qb[1, 0, 7] = bad
+        c.attn(qb, kp, vp, o)
+        torch.cuda.synchronize()
+        assert bool(torch.isnan(o[1, 0]).all()), bad
+        good = torch.ones(n, 2, dtype=torch.bool)
+        good[1, 0] = False
+        (_, rows, ref, mag), = expect_attn(c, oc, q, kp, vp, want, SCALE)
+        got = f64(o)[rows]
+        keep = good.numpy()
+        assert_attn(got[keep], ref[keep], mag[keep], "others", 40.0)
+    if max_new == 4:
+        at = kv + 2                  # the third row's own position
+        kp[oc.table[0][at // 16], 1, at % 16, 3] = float("nan")
+        c.attn(q, kp, vp, o)
+        torch.cuda.synchronize()
+        nan = torch.isnan(o).all(-1).cpu()
+        assert nan.tolist() == [[False, False], [False, False],
+                                [False, True], [False, True]]
+        assert bool(torch.isfinite(o[~nan.cuda()]).all())
+    assert wan.device_status() == 0

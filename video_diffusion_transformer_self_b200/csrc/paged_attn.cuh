@@ -113,7 +113,9 @@ struct JoinAcc {
   // come with one load a lane, their O rows with batches of independent
   // loads, the first of them before the maxima are there (loads under a
   // condition ran one after the other: 25 parts took 13 us instead of 4).
-  // A part without keys is loaded too, whatever it holds, and dropped.
+  // A part without keys (a sum of exactly 0; any other holds its maximum's
+  // weight of 1) is loaded too, whatever it holds, and dropped.  A NaN sum
+  // goes into the row's, and so into the result.
   template <typename RowOf, typename Has>
   __device__ __forceinline__ void add_all(int n, int lane, const PagedArgs& a,
                                           RowOf row_of, Has has) {
@@ -129,15 +131,15 @@ struct JoinAcc {
       float2 ml = make_float2(-INFINITY, 0.f);
       if (lane < cnt && has(k0 + lane)) ml = a.part_ml[row_of(k0 + lane)];
       load(0);
-      if (!(ml.y > 0.f)) ml = make_float2(-INFINITY, 0.f);
-      float top = ml.x;
+      const bool some = ml.y != 0.f;
+      if (!__any_sync(0xffffffffu, some)) continue;
+      float top = some ? ml.x : -INFINITY;
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1)
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      if (top == -INFINITY) continue;
       const float mn = fmaxf(m, top);
       const float w0 = m == -INFINITY ? 0.f : ex2(m - mn);
-      const float w = ml.x == -INFINITY ? 0.f : ex2(ml.x - mn);
+      const float w = some ? ex2(ml.x - mn) : 0.f;
       float sum = ml.y * w;
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1)
@@ -163,7 +165,7 @@ struct JoinAcc {
     }
   }
   __device__ __forceinline__ void write(__nv_bfloat16* dst, int lane) const {
-    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
     reinterpret_cast<uint2*>(dst)[lane] =
         make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv),
                    pack_bf16x2(acc.z * inv, acc.w * inv));
