@@ -704,7 +704,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           const bool need = mx > m_run + RESCALE_LOG2;
           if (__any_sync(0xffffffffu, need)) {
             const float m_new = need ? mx : m_run;
-            const float alpha = ex2(m_run - m_new);
+            // (a row without keys so far: -inf - -inf, and the minimum of NaN
+            // and 0 is 0, so its factor is 1)
+            const float alpha = ex2(fminf(m_run - m_new, 0.f));
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
               float o[32];
@@ -1256,7 +1258,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::THREADS, 1)
       if (lane == 0) mbar_arrive(&bar[MCHAIN + qd]);
       if (__any_sync(0xffffffffu, need)) {
         // O holds blocks 0 .. j-1 at m_prev once P V(j-1) has landed
-        const float alpha = ex2(m_prev - m_j);
+        // (a row without keys so far: factor 1, as in attn_fwd_kernel)
+        const float alpha = ex2(fminf(m_prev - m_j, 0.f));
         ok = wait_warp(&bar[PVDONE + (j - 1) % NSLOT], ((j - 1) / NSLOT) & 1,
                        abort_flag, status);
         if (!ok) break;
