@@ -40,3 +40,26 @@ def test_rows_without_keys_beside_rows_whose_maximum_moves(chunk, n_split,
                                     * k.float().norm(dim=-1).max())
     assert_attn(f64(o), want, mag, "chunk %d, %d ranges" % (chunk, n_split),
                 score_sum)
+
+
+def test_scratch_of_a_call_on_another_stream_is_not_handed_out_meanwhile():
+    L, chunk, n_split = 2048, 1024, 2
+    q, k, v = (cuda(inputs.randn_bf16((1, L, 2, 128), 90 + i))
+               for i in range(3))
+    o = torch.empty_like(q)
+    want = torch.empty_like(q)
+    wan.block_causal_attn(q, k, v, want, chunk, split=n_split)
+    need = wan.block_causal_workspace_bytes(1, L, 2, n_split)
+    side = torch.cuda.Stream()
+    # (the fill kernel is loaded now: loading waits for the device)
+    assert bool((torch.full((need,), 77, dtype=torch.uint8,
+                            device="cuda") == 77).all())
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(100_000_000)      # some 50 ms before the kernels
+    wan.block_causal_attn(q, k, v, o, chunk, split=n_split, stream=side)
+    later = torch.full((need,), 77, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    assert bool((later == 77).all())
+    assert torch.equal(o, want)

@@ -415,7 +415,11 @@ def block_causal_attn(q, k, v, o, chunk_tokens, q_offset=0,
         need = block_causal_workspace_bytes(B, Lq, H, n_split)
         if workspace is None:
             import torch
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+            # on the call's own stream: freed on return, it goes back to that
+            # stream's memory, behind the kernels that use it
+            with torch.cuda.stream(stream):
+                workspace = torch.empty(need, dtype=torch.uint8,
+                                        device=q.device)
         if not workspace.is_contiguous() or \
                 workspace.numel() * workspace.element_size() < need:
             raise ValueError("workspace must be a contiguous tensor of at "
