@@ -145,3 +145,20 @@ def test_rows_that_are_not_finite_stay_so_however_they_are_cut(max_new, kv):
                                 [False, True], [False, True]]
         assert bool(torch.isfinite(o[~nan.cuda()]).all())
     assert wan.device_status() == 0
+
+
+@pytest.mark.parametrize("max_new", [2 ** 31, 2 ** 32 + 5, 10 ** 18])
+def test_max_new_past_32_bits_is_no_limit(max_new):
+    c, oc = make([(8, 8, 64, 0)], (60, 8, 8), 60, 32, 40, 2, 2, 300, max_new)
+    want = step(c, oc, [300])
+    assert c.status.tolist() == [0] and c.q_lens.tolist() == [300]
+    kp, vp = c.new_pools()
+    kp.normal_()
+    vp.normal_()
+    q = rows_bf16(300, 2, 5).cuda()
+    o = torch.zeros_like(q)
+    c.attn(q, kp, vp, o)
+    torch.cuda.synchronize()
+    assert wan.device_status() == 0
+    (_, rows, ref, mag), = expect_attn(c, oc, q, kp, vp, want, SCALE)
+    assert_attn(f64(o)[rows], ref, mag, "max_new %d" % max_new, 30.0)

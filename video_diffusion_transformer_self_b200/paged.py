@@ -160,7 +160,8 @@ class PagedCache:
                     self.block_table, self.free_ring, self.ring_state,
                     self.q_start, self.q_lens, self.status, self.tokens,
                     self._work)))
-        d.max_new = self.max_new
+        # (ctypes would cut off what passes 32 bits)
+        d.max_new = min(self.max_new, 2 ** 31 - 1)
         return d
 
     def _check(self, shape, name, t):
