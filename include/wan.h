@@ -364,9 +364,15 @@ size_t wan_paged_work_bytes(int n_streams);
  *      it brings more than max_new; nothing of it changes.
  *   3. The others take pages from the ring in the order of the streams, up
  *      to the first that the free pages do not suffice for: it and all
- *      after it are refused with WAN_ENOSPACE (they keep what they have and
- *      can be planned again).  Pages given back in 1. count as free.
+ *      after it are refused with WAN_ENOSPACE (they keep their length and
+ *      the pages that 1. left them, which is all that their next tokens see,
+ *      and can be planned again).  Pages given back in 1. count as free.
  * A refused stream's rows keep their place in the packing with slot -1.
+ * Positions count from a stream's start and table entries given back are not
+ * used again, so a window bounds a stream's pages, not its length: at the end
+ * of the grid (1,024 frames at most) or of max_pages it is refused with
+ * WAN_EINVAL.  It can then be ended and started anew, its last chunks written
+ * again as its first tokens.
  * Writes kv_lens (including the new tokens), first_pages, block_table,
  * free_ring, ring_state, q_start, q_lens, status, tokens (all token_cap of
  * them) and work.  A free ring starts as pages 0 .. n_pages - 1 with

@@ -159,8 +159,9 @@ __device__ __forceinline__ int find_stream(const int* incl, int n, int x) {
   return lo;
 }
 
-// The least weight of a piece that a cut leaves (a piece costs its start, its
-// partial result and the join of it, about six key blocks).
+// How far a cut stays from the ends of the unit it falls into (a piece costs
+// its start, its partial result and the join of it, about six key blocks).
+// Two cuts inside one unit may be closer: a CTA that lacks little gets little.
 constexpr int kMinPiece = 64;
 // Where there are more CTAs than units, down to a quarter of it for very few
 // units: 2 units of 80 blocks 36 us with 64, 23 with 16; 12 of 260 51 and 45;

@@ -692,9 +692,13 @@ __global__ void __launch_bounds__(128)
 // fp32 partial results instead, joined by paged_tile_join.
 // Bound, like attn_fwd_kernel, by each tile's chain of softmax and matrix
 // products (tensor pipe 61 % active), and by the power cap in long calls.
-// Measured: 4,680 rows x 12 heads over 32,760 keys 740 to 860 us by clock
-// (1,095 to 1,270 TFLOP/s), x 40 heads over 65,520 keys 5.0 to 5.6 ms (1,120
+// Measured: 4,680 rows x 12 heads over 32,760 keys 740 to 900 us by clock
+// (1,050 to 1,270 TFLOP/s), x 40 heads over 65,520 keys 5.0 to 5.75 ms (1,090
 // to 1,250); with units of 256 rows a CTA in turn they took 965 us and 6.0 ms.
+// 20 to 400 rows of six streams x 12 heads take 83 us: 26 key blocks a CTA of
+// about 1.9 us, the rest starts and ends of units, partial results (128 KB a
+// piece) and their join.  The kernel needs 44 bytes of spill stores and 72 of
+// loads a thread, which attn_fwd_kernel does without.
 // Rows stored from registers instead of through the Q buffer, the next unit's
 // scores started meanwhile: small calls 4 % shorter to 6 % longer, long ones
 // unchanged, two to three registers spilled.
