@@ -69,7 +69,7 @@ def test_plan_stops_at_the_first_that_lacks_pages():
     assert_plan(c, oc, want)
 
 
-# 1 CTA up to 2,048 records, a cluster beyond; up to the most streams
+# one stream to the most, a record to tens of thousands
 @pytest.mark.parametrize("R,cap,hi,seed", [
     (1, 1, 1, 0), (1, 5000, 5000, 1), (33, 2048, 90, 2), (33, 2049, 90, 3),
     (1000, 9000, 20, 4), (1024, 40000, 60, 5), (1024, 2000, 3, 6)])
