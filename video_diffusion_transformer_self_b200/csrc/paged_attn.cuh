@@ -693,7 +693,7 @@ __global__ void __launch_bounds__(128)
 // Bound, like attn_fwd_kernel, by each tile's chain of softmax and matrix
 // products (tensor pipe 61 % active), and by the power cap in long calls.
 // Measured: 4,680 rows x 12 heads over 32,760 keys 740 to 900 us by clock
-// (1,050 to 1,270 TFLOP/s), x 40 heads over 65,520 keys 5.0 to 5.75 ms (1,090
+// (1,050 to 1,270 TFLOP/s), x 40 heads over 65,520 keys 5.0 to 5.85 ms (1,075
 // to 1,250); with units of 256 rows a CTA in turn they took 965 us and 6.0 ms.
 // 20 to 400 rows of six streams x 12 heads take 83 us: 26 key blocks a CTA of
 // about 1.9 us, the rest starts and ends of units, partial results (128 KB a
