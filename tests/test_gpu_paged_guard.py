@@ -162,3 +162,41 @@ def test_max_new_past_32_bits_is_no_limit(max_new):
     assert wan.device_status() == 0
     (_, rows, ref, mag), = expect_attn(c, oc, q, kp, vp, want, SCALE)
     assert_attn(f64(o)[rows], ref, mag, "max_new %d" % max_new, 30.0)
+
+
+@pytest.mark.parametrize("max_new,steps", [
+    (16, [[5, 17, 16, 0, 1], [16, 3, 30, 2, -1], [1, 16, 0, 40, 9]]),
+    (300, [[30, 301, 129, 0, 1], [257, 3, 400, 300, -1],
+           [300, 16, 0, 333, 90]])])
+def test_rows_of_no_stream_may_hold_anything(max_new, steps):
+    """Streams refused in the middle of the packing and rows behind the last
+    one, all NaN: the others' results are whole, theirs stay as they were."""
+    cap = max(sum(max(n, 0) for n in s) for s in steps) + 9
+    c, oc = make([(8, 8, 64, 0), (8, 8, 1, 100)] * 2 + [(8, 8, 20, 30)],
+                 (60, 8, 8), 200, 16, 70, 4, 2, cap, max_new)
+    kp, vp = c.new_pools()
+    w4, w2 = torch.ones(512, device="cuda"), torch.ones(256, device="cuda")
+    table = wan.rope3d_table(c.grid)
+    for i, new in enumerate(steps):
+        want = step(c, oc, new)
+        assert any(s == wan.WAN_EINVAL for s in want[2])
+        taken = torch.zeros(cap, dtype=torch.bool)
+        for at, n in zip(want[0], want[1]):
+            taken[at:at + n] = True
+        q, k, v = (rows_bf16(cap, h, 10 * i + j)
+                   for j, h in enumerate((4, 2, 2)))
+        for t in (q, k, v):
+            t[~taken] = float("nan")
+        q, k, v = q.cuda(), k.cuda(), v.cuda()
+        c.write(q, k, v, w4, w2, table, kp, vp)
+        o = rows_bf16(cap, 4, 10 * i + 5).cuda()
+        rest = o.clone()
+        c.attn(q, kp, vp, o)
+        torch.cuda.synchronize()
+        assert wan.device_status() == 0
+        assert bool(torch.isfinite(kp).all() and torch.isfinite(vp).all())
+        assert torch.equal(torch.isnan(q).all(-1).all(-1).cpu(), ~taken)
+        assert torch.equal(o[~taken.cuda()], rest[~taken.cuda()])
+        for r, rows, ref, mag in expect_attn(c, oc, q, kp, vp, want, SCALE):
+            assert_attn(f64(o)[rows], ref, mag, "step %d stream %d" % (i, r),
+                        40.0)
